@@ -330,6 +330,97 @@ RWKV7_API int rwkv7_step_timeline(rwkv7_ctx *ctx, const int32_t *d_slots, const 
  * three launches instead of one (with the same results). */
 RWKV7_API int32_t rwkv7_step_kernel_count(const rwkv7_ctx *ctx, int32_t B, int32_t with_sampling);
 
+/* ---------------------------------------------------------------------------
+ * Microscaled formats: blocks of 32 consecutive values of a row that share one
+ * power of two, as the Open Compute Project's microscaling specification lays
+ * them down.  The articles' roadmap names quantised weights and a prefix-state
+ * cache ("正在演进" list, "边界与后续路线"); these calls are the 4-bit step beyond
+ * the int8 weights, and entries a quarter or an eighth of a state's size.
+ *
+ *   MXFP4   sign and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6, times the block's power:
+ *           the least 2^e, e >= -127, with max |x| <= 6 * 2^e
+ *   MXINT8  q / 64, q = -127 .. 127, times the block's power: the least 2^e,
+ *           -126 <= e <= 127, with max |x| <= 127/64 * 2^e
+ *
+ * Values go to the nearest of the format, ties to the even code.  A block that
+ * holds an infinity or a NaN reads back as NaN throughout.
+ *
+ * These calls need no ctx: the caller owns every buffer, all on the current
+ * device.  They allocate nothing, launch on cuda_stream (NULL: the legacy default
+ * stream) and return RWKV7_OK, RWKV7_EINVAL or RWKV7_ECUDA; err_msg, if not NULL,
+ * receives a text ("" on success) valid until the same thread's next call.  They
+ * may be captured into a graph.
+ * ------------------------------------------------------------------------- */
+#define RWKV7_F32 0
+#define RWKV7_F16 1
+#define RWKV7_BF16 2
+#define RWKV7_MXFP4 0
+#define RWKV7_MXINT8 1
+#define RWKV7_ACT_NONE 0
+#define RWKV7_ACT_RELU2 1              /* y = max(y, 0)^2, NaN kept */
+#define RWKV7_MX_MAX_DIM (1 << 24)     /* rows and columns of an MXFP4 matrix */
+#define RWKV7_STATES_MAX_PAIRS 1024    /* (slot, entry) pairs of one call */
+
+/* Bytes of an MXFP4 matrix: 17,408 for each tile of 128 rows x 256 columns,
+ * ragged ones padded.  0 for a size out of range. */
+RWKV7_API size_t rwkv7_mx4_bytes(int64_t rows, int64_t cols);
+
+/* Quantise rows: d_x [rows][cols] of type dtype (RWKV7_F32 / F16 / BF16), row
+ * stride ld elements (any; rows that start on 16-byte boundaries are read
+ * fastest), into d_mx (rwkv7_mx4_bytes(rows, cols) bytes, 16-byte aligned).
+ * rows may be 0. */
+RWKV7_API int rwkv7_mx4_quantize(const void *d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                 void *d_mx, void *cuda_stream, const char **err_msg);
+
+/* The values an MXFP4 matrix stands for, rounded to dtype (exact in fp32 and,
+ * inside its range, in fp16 and bf16), into d_y at row stride ld. */
+RWKV7_API int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y, int32_t dtype,
+                                   int64_t ld, void *cuda_stream, const char **err_msg);
+
+/* y[b][n] = act(sum_k x[b][k] w[n][k]), x and w the values of MXFP4 matrices
+ * [B][K] and [N][K], fp32 sums, the result rounded once to y_dtype (row stride
+ * ldy elements).  d_x_mx holds x; if d_x is not NULL, its rows (x_dtype, row
+ * stride ldx) are quantised into d_x_mx first.  B may be 0.  d_err: a device
+ * word the caller zeroed; bit 8 is set if a bounded wait in the kernel gave up
+ * (y is then undefined). */
+RWKV7_API int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx, int64_t B,
+                               const void *d_w_mx, int64_t N, int64_t K, void *d_y, int32_t y_dtype, int64_t ldy,
+                               int32_t activation, uint32_t *d_err, void *cuda_stream, const char **err_msg);
+
+/* Bytes of one slot's state in a cache of the given format: n_layer * n_head *
+ * 4096 codes, their powers, and both token-shift states as fp32.  0 for bad
+ * arguments. */
+RWKV7_API size_t rwkv7_state_entry_bytes(int32_t n_layer, int32_t n_head, int32_t format);
+
+/* Save the states of n slots into entries of d_cache (n_entries times
+ * rwkv7_state_entry_bytes bytes, 16-byte aligned), or load entries into slots:
+ * pair i is slot d_slots[i] and entry d_entries[i] (device int32 [n],
+ * 0 <= n <= RWKV7_STATES_MAX_PAIRS).  The pool is fp32, as the ctx keeps it: d_wkv
+ * [n_layer][n_slots][n_head][64][64], d_shift_att and d_shift_ffn
+ * [n_layer][n_slots][64 * n_head], 16-byte aligned.  The wkv states are quantised
+ * along their rows (the key channels), the shift states kept exactly.  Several
+ * pairs may read the same slot or entry.  Where two pairs write the same one the
+ * first is carried out, the others are not, and bit 4 is set in *d_err (a device
+ * word the caller zeroed); an index out of range sets bit 1 and its pair is left
+ * out. */
+RWKV7_API int rwkv7_states_save(const float *d_wkv, const float *d_shift_att, const float *d_shift_ffn,
+                                int32_t n_layer, int32_t n_head, int32_t n_slots, const int32_t *d_slots,
+                                const int32_t *d_entries, int32_t n, void *d_cache, int32_t n_entries, int32_t format,
+                                uint32_t *d_err, void *cuda_stream, const char **err_msg);
+RWKV7_API int rwkv7_states_load(float *d_wkv, float *d_shift_att, float *d_shift_ffn, int32_t n_layer, int32_t n_head,
+                                int32_t n_slots, const int32_t *d_slots, const int32_t *d_entries, int32_t n,
+                                const void *d_cache, int32_t n_entries, int32_t format, uint32_t *d_err,
+                                void *cuda_stream, const char **err_msg);
+
+/* The same between the ctx's own slots and a cache the caller owns, on the ctx's
+ * stream; bad or repeated indices are latched and reported by rwkv7_synchronize.
+ * A loaded slot's occurrence counts and draw counter restart, as with
+ * rwkv7_slot_copy. */
+RWKV7_API int rwkv7_slots_save(rwkv7_ctx *ctx, const int32_t *d_slots, const int32_t *d_entries, int32_t n,
+                               void *d_cache, int32_t n_entries, int32_t format);
+RWKV7_API int rwkv7_slots_load(rwkv7_ctx *ctx, const int32_t *d_slots, const int32_t *d_entries, int32_t n,
+                               const void *d_cache, int32_t n_entries, int32_t format);
+
 #ifdef __cplusplus
 }
 #endif

@@ -80,6 +80,21 @@ SIGNATURES = {
                                       C.c_void_p, C.c_int32, C.POINTER(C.c_int32)]),
 }
 
+_I32, _I64 = C.c_int32, C.c_int64
+_MSG = C.POINTER(C.c_char_p)
+_STATES = [_VP, _VP, _VP, _I32, _I32, _I32, _VP, _VP, _I32, _VP, _I32, _I32, _VP, _VP, _MSG]
+SIGNATURES.update({
+    "rwkv7_mx4_bytes": (C.c_size_t, [_I64, _I64]),
+    "rwkv7_mx4_quantize": (C.c_int, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _MSG]),
+    "rwkv7_mx4_dequantize": (C.c_int, [_VP, _I64, _I64, _VP, _I32, _I64, _VP, _MSG]),
+    "rwkv7_mx4_linear": (C.c_int, [_VP, _I32, _I64, _VP, _I64, _VP, _I64, _I64, _VP, _I32, _I64, _I32, _VP, _VP, _MSG]),
+    "rwkv7_state_entry_bytes": (C.c_size_t, [_I32, _I32, _I32]),
+    "rwkv7_states_save": (C.c_int, _STATES),
+    "rwkv7_states_load": (C.c_int, _STATES),
+    "rwkv7_slots_save": (C.c_int, [_VP, _VP, _VP, _I32, _VP, _I32, _I32]),
+    "rwkv7_slots_load": (C.c_int, [_VP, _VP, _VP, _I32, _VP, _I32, _I32]),
+})
+
 SAMPLE_STATIC_MAX_ELEMS = 1 << 22
 
 PROF_CLASSES = ["embed", "ln_mix", "gemm_proj", "gemm_lora", "wkv", "gemm_out", "gemm_key", "gemm_value",
@@ -272,6 +287,26 @@ class Rwkv7:
     def slot_copy(self, src: int, dst: int):
         self._check(self.lib.rwkv7_slot_copy(self.h, src, dst))
 
+    def slots_save(self, cache: "StateCache", slots, entries):
+        """rwkv7_slots_save: keep the states of `slots` in `entries` of a StateCache
+        of this model's layers and heads (int32 CUDA tensors of equal length)."""
+        n = self._pairs(cache, slots, entries)
+        self._check(self.lib.rwkv7_slots_save(self.h, slots.data_ptr(), entries.data_ptr(), n, cache.data.data_ptr(),
+                                              cache.n_entries, cache.format))
+
+    def slots_load(self, cache: "StateCache", entries, slots):
+        """rwkv7_slots_load: put the kept states of `entries` into `slots`, whose
+        occurrence counts and draw counters restart."""
+        n = self._pairs(cache, slots, entries)
+        self._check(self.lib.rwkv7_slots_load(self.h, slots.data_ptr(), entries.data_ptr(), n, cache.data.data_ptr(),
+                                              cache.n_entries, cache.format))
+
+    def _pairs(self, cache, slots, entries):
+        if (cache.n_layer, cache.n_head) != (self.dims.n_layer, self.dims.n_head):
+            raise ValueError("the cache was made for another number of layers or heads")
+        from .mx import _pair_count
+        return _pair_count(slots, entries, cache.data.device)
+
     def set_sampling(self, slot: int, temperature=1.0, top_p=0.3, top_k=0, presence=0.0,
                      frequency=1.0, penalty_decay=0.996, seed=0, greedy=False):
         sp = Sampling(temperature, top_p, top_k, presence, frequency, penalty_decay, seed, int(bool(greedy)))
@@ -384,5 +419,17 @@ class Rwkv7:
         return tuple(x.value for x in p)
 
 
-__all__ = ["Rwkv7", "RWKV7Error", "Config", "Sampling", "load_library", "build", "LIB_PATH",
+_MX = ("MX4Matrix", "StateCache", "mx4_check", "mx4_empty", "mx4_linear", "mx4_quantize")
+
+
+def __getattr__(name):
+    """The microscaled operators (mx.py), imported with torch on first use."""
+    if name not in _MX:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import mx
+    globals().update({n: getattr(mx, n) for n in _MX})
+    return globals()[name]
+
+
+__all__ = [*_MX, "Rwkv7", "RWKV7Error", "Config", "Sampling", "load_library", "build", "LIB_PATH",
            "SIGNATURES", "MAX_STEP_BATCH", "PROF_CLASSES", "set_device_allocator"]

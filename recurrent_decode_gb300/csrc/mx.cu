@@ -1,0 +1,406 @@
+// mx.cu -- MXFP4 quantisation of rows and its inverse, and slot states saved to
+// and loaded from a cache of MXINT8 or MXFP4 entries (formats: mx.cuh).
+//
+// All four kernels move each value once and do a handful of operations on it, so
+// HBM bounds them; eight neighbouring values belong to one lane and a block of 32
+// to four, whose largest value takes two shuffles.
+#include <cstdio>
+#include <cstring>
+
+#include "../../include/rwkv7.h"
+#include "mx.cuh"
+
+namespace rk {
+
+template <int T>
+struct MxElem;
+template <>
+struct MxElem<MX_F32> {
+    using type = float;
+    static __device__ __forceinline__ float up(float v) { return v; }
+    static __device__ __forceinline__ float down(float v) { return v; }
+};
+template <>
+struct MxElem<MX_F16> {
+    using type = __half;
+    static __device__ __forceinline__ float up(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+};
+template <>
+struct MxElem<MX_BF16> {
+    using type = __nv_bfloat16;
+    static __device__ __forceinline__ float up(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+};
+
+struct MxRowsParams {
+    void *x;  // [rows] at ld
+    int64_t rows, cols, ld;
+    uint8_t *mx;
+    int64_t kt;  // column tiles
+    int vec;     // rows start on 16-byte boundaries
+};
+
+constexpr int MXQ_THREADS = 256;
+
+// One warp per (row, column tile): eight values a lane.
+template <int T>
+__global__ void __launch_bounds__(MXQ_THREADS) mx4_quantize_kernel(const MxRowsParams p) {
+    using E = typename MxElem<T>::type;
+    const int64_t line = (int64_t)blockIdx.x * (MXQ_THREADS / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (line >= p.rows * p.kt) return;
+    const int64_t r = line / p.kt, t = line % p.kt;
+    const int64_t c0 = t * MX_TILE_K + lane * 8;
+    const E *src = (const E *)p.x + r * p.ld + c0;
+    float v[8];
+    if (p.vec && c0 + 8 <= p.cols) {
+        alignas(16) E u[8];
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(u) / 16; ++i) ((uint4 *)u)[i] = ((const uint4 *)src)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = MxElem<T>::up(u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c0 + i < p.cols ? MxElem<T>::up(src[i]) : 0.0f;
+    }
+    const uint32_t s = mx_scale<MXFP4>(mx_quad_top(v));
+    const float f = s == 255u ? 0.0f : mx_inverse(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = s == 255u ? 0.0f : v[i] * f;
+    uint8_t *tile = p.mx + ((r / MX_TILE_M) * p.kt + t) * MX_TILE_BYTES;
+    const int rr = (int)(r % MX_TILE_M), blk = lane >> 2;
+    *(uint32_t *)(tile + MX_SCALE_BYTES + rr * 128 + ((blk ^ (rr & 7)) << 4) + (lane & 3) * 4) = fp4_pack8(v);
+    if ((lane & 3) == 0) tile[(blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4 + (blk & 3)] = (uint8_t)s;
+}
+
+template <int T>
+__global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRowsParams p) {
+    using E = typename MxElem<T>::type;
+    const int64_t line = (int64_t)blockIdx.x * (MXQ_THREADS / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (line >= p.rows * p.kt) return;
+    const int64_t r = line / p.kt, t = line % p.kt;
+    const int64_t c0 = t * MX_TILE_K + lane * 8;
+    const uint8_t *tile = p.mx + ((r / MX_TILE_M) * p.kt + t) * MX_TILE_BYTES;
+    const int rr = (int)(r % MX_TILE_M), blk = lane >> 2;
+    const uint32_t code = *(const uint32_t *)(tile + MX_SCALE_BYTES + rr * 128 + ((blk ^ (rr & 7)) << 4) + (lane & 3) * 4);
+    const uint32_t s = tile[(blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4 + (blk & 3)];
+    float v[8];
+    fp4_unpack8(code, v);
+    const float f = s == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s);
+    alignas(16) E u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = MxElem<T>::down(v[i] * f);
+    E *dst = (E *)p.x + r * p.ld + c0;
+    if (p.vec && c0 + 8 <= p.cols) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(u) / 16; ++i) ((uint4 *)dst)[i] = ((const uint4 *)u)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c0 + i < p.cols) dst[i] = u[i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// States.  An entry holds one slot's state: codes of wkv [L][H][64][64], then
+// the powers [L][H][128] (blocks of 32 along a state row), then the two shift
+// states [L][2][d] as they are (3 % of the fp32 state; every later token mixes
+// them in unscaled, so they stay exact).
+// ---------------------------------------------------------------------------
+constexpr int MXS_THREADS = 256;
+constexpr int MX_HEAD = HS * HS;  // values of one head's state
+
+struct MxStateParams {
+    float *wkv, *att, *ffn;  // [L][n_slots][H][64][64], [L][n_slots][d] twice
+    int L, H, n_slots, n_entries;
+    const int32_t *slots, *entries;
+    uint8_t *cache;
+    int64_t entry_bytes;
+    uint32_t *err;
+    // load into a ctx: what a slot restarts with its new state (else null)
+    float *occ;
+    unsigned long long *ndraw;
+    int V;
+};
+
+__host__ __device__ constexpr int64_t mx_codes(int64_t heads, int fmt) { return heads * (fmt == MXINT8 ? MX_HEAD : MX_HEAD / 2); }
+
+// Whether this CTA's pair i is one to carry out: both indices in range, and no
+// earlier pair with the same target (one of two copies into the same place would
+// win by chance: the first does, the others are reported).
+__device__ __forceinline__ bool mx_pair_ok(const int32_t *target, int ntarget, int32_t other, int nother, int i,
+                                           uint32_t *err, bool speak) {
+    const int32_t t = target[i];
+    int dup = 0;
+    for (int j = threadIdx.x; j < i; j += MXS_THREADS) dup |= target[j] == t;
+    dup = __syncthreads_or(dup);
+    const bool in = t >= 0 && t < ntarget && other >= 0 && other < nother;
+    if (speak && threadIdx.x == 0 && (dup || !in)) atomicOr(err, in ? ERR_DUP : ERR_SLOT);
+    return in && !dup;
+}
+
+// CTA (h, i): head h (of all layers' heads) of pair i; two groups of eight values a thread.
+template <int FMT, bool SAVE>
+__global__ void __launch_bounds__(MXS_THREADS) mx_state_kernel(const MxStateParams p) {
+    const int hl = blockIdx.x, i = blockIdx.y;
+    const int layer = hl / p.H, head = hl % p.H;
+    const int32_t slot = p.slots[i], entry = p.entries[i];
+    if (!(SAVE ? mx_pair_ok(p.entries, p.n_entries, slot, p.n_slots, i, p.err, hl == 0)
+               : mx_pair_ok(p.slots, p.n_slots, entry, p.n_entries, i, p.err, hl == 0)))
+        return;
+    const int64_t heads = (int64_t)p.L * p.H;
+    uint8_t *codes = p.cache + (int64_t)entry * p.entry_bytes + mx_codes(hl, FMT);
+    uint8_t *scales = p.cache + (int64_t)entry * p.entry_bytes + mx_codes(heads, FMT) + (int64_t)hl * (MX_HEAD / MX_BLOCK);
+    float *shift = (float *)(p.cache + (int64_t)entry * p.entry_bytes + mx_codes(heads, FMT) +
+                             heads * (MX_HEAD / MX_BLOCK)) + (int64_t)layer * 2 * p.H * HS;
+    float *st = p.wkv + (((int64_t)layer * p.n_slots + slot) * p.H + head) * MX_HEAD;
+    if (threadIdx.x < 2 * HS / 4) {  // the head's 64 channels of both shift states
+        const int which = threadIdx.x / (HS / 4), c = head * HS + (threadIdx.x % (HS / 4)) * 4;
+        float4 *a = (float4 *)((which ? p.ffn : p.att) + ((int64_t)layer * p.n_slots + slot) * p.H * HS + c);
+        float4 *b = (float4 *)(shift + (int64_t)which * p.H * HS + c);
+        if (SAVE) *b = *a;
+        else *a = *b;
+    }
+    if (!SAVE && p.occ) {
+        const int64_t a = (int64_t)p.V * hl / heads, b = (int64_t)p.V * (hl + 1) / heads;
+        for (int64_t k = a + threadIdx.x; k < b; k += MXS_THREADS) p.occ[(int64_t)slot * p.V + k] = 0.0f;
+        if (hl == 0 && threadIdx.x == 0) p.ndraw[slot] = 0ull;
+    }
+#pragma unroll
+    for (int g = threadIdx.x; g < MX_HEAD / 8; g += MXS_THREADS) {
+        float v[8];
+        if (SAVE) {
+            *(float4 *)&v[0] = ((const float4 *)st)[2 * g];
+            *(float4 *)&v[4] = ((const float4 *)st)[2 * g + 1];
+            const uint32_t s = mx_scale<FMT>(mx_quad_top(v));
+            const float f = s == 255u ? 0.0f : mx_inverse(s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = s == 255u ? 0.0f : v[j] * f;
+            if (FMT == MXFP4) {
+                ((uint32_t *)codes)[g] = fp4_pack8(v);
+            } else {
+                uint32_t w[2] = {0, 0};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int q = min(127, max(-127, __float2int_rn(v[j] * 64.0f)));
+                    w[j >> 2] |= ((uint32_t)q & 255u) << (8 * (j & 3));
+                }
+                ((uint2 *)codes)[g] = make_uint2(w[0], w[1]);
+            }
+            if ((g & 3) == 0) scales[g >> 2] = (uint8_t)s;
+        } else {
+            const uint32_t s = scales[g >> 2];
+            const float f = s == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s);
+            if (FMT == MXFP4) {
+                fp4_unpack8(((const uint32_t *)codes)[g], v);
+            } else {
+                const uint2 w = ((const uint2 *)codes)[g];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * (1.0f / 64.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= f;
+            ((float4 *)st)[2 * g] = *(float4 *)&v[0];
+            ((float4 *)st)[2 * g + 1] = *(float4 *)&v[4];
+        }
+    }
+}
+
+}  // namespace rk
+
+// ---------------------------------------------------------------------------
+// C entry points
+// ---------------------------------------------------------------------------
+using namespace rk;
+namespace {
+
+thread_local char g_mx_msg[192];
+
+int mx_fail(const char **err_msg, int code, const char *fmt, long long a = 0, long long b = 0) {
+    snprintf(g_mx_msg, sizeof g_mx_msg, fmt, a, b);
+    if (err_msg) *err_msg = g_mx_msg;
+    return code;
+}
+int mx_done(const char **err_msg, const char *what, cudaError_t e) {
+    if (e == cudaSuccess) return RWKV7_OK;
+    snprintf(g_mx_msg, sizeof g_mx_msg, "%s: %s", what, cudaGetErrorString(e));
+    if (err_msg) *err_msg = g_mx_msg;
+    return RWKV7_ECUDA;
+}
+bool mx_size_ok(int64_t rows, int64_t cols) { return rows >= 0 && cols >= 1 && rows <= RWKV7_MX_MAX_DIM && cols <= RWKV7_MX_MAX_DIM; }
+
+int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, const void *mx,
+                  const char **err_msg) {
+    if (err_msg) *err_msg = "";
+    if (!mx_size_ok(rows, cols))
+        return mx_fail(err_msg, RWKV7_EINVAL, "rows must be >= 0 and cols >= 1, both at most 2^24 (rows=%lld, cols=%lld)",
+                       rows, cols);
+    if (dtype < RWKV7_F32 || dtype > RWKV7_BF16) return mx_fail(err_msg, RWKV7_EINVAL, "unknown dtype %lld", dtype);
+    if (rows > 1 && ld < cols) return mx_fail(err_msg, RWKV7_EINVAL, "row stride %lld is below cols=%lld", ld, cols);
+    if (rows > 0 && (!x || !mx)) return mx_fail(err_msg, RWKV7_EINVAL, "null pointer argument");
+    const int size = dtype == RWKV7_F32 ? 4 : 2;
+    if ((uintptr_t)x % size) return mx_fail(err_msg, RWKV7_EINVAL, "the rows' pointer is not aligned to its type");
+    if ((uintptr_t)mx & 15u) return mx_fail(err_msg, RWKV7_EINVAL, "the MXFP4 matrix must be 16-byte aligned");
+    p.x = const_cast<void *>(x);
+    p.rows = rows;
+    p.cols = cols;
+    p.ld = ld;
+    p.mx = static_cast<uint8_t *>(const_cast<void *>(mx));
+    p.kt = (cols + MX_TILE_K - 1) / MX_TILE_K;
+    p.vec = (uintptr_t)x % 16 == 0 && (rows <= 1 || ld * size % 16 == 0);
+    return RWKV7_OK;
+}
+
+cudaError_t mx_launch_rows(const void *kernel, MxRowsParams &p, const LaunchCfg &lc) {
+    const int64_t lines = p.rows * p.kt, per = MXQ_THREADS / 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((lines + per - 1) / per));
+    cfg.blockDim = dim3(MXQ_THREADS);
+    cfg.stream = lc.stream;
+    void *args[] = {&p};
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+const void *mx_quantize_fn(int dtype) {
+    return dtype == MX_F32   ? (const void *)mx4_quantize_kernel<MX_F32>
+           : dtype == MX_F16 ? (const void *)mx4_quantize_kernel<MX_F16>
+                             : (const void *)mx4_quantize_kernel<MX_BF16>;
+}
+const void *mx_dequantize_fn(int dtype) {
+    return dtype == MX_F32   ? (const void *)mx4_dequantize_kernel<MX_F32>
+           : dtype == MX_F16 ? (const void *)mx4_dequantize_kernel<MX_F16>
+                             : (const void *)mx4_dequantize_kernel<MX_BF16>;
+}
+
+int mx_states(bool save, MxStateParams &p, int32_t n, int32_t format, void *stream, const char **err_msg) {
+    if (err_msg) *err_msg = "";
+    if (p.L < 1 || p.H < 1 || p.n_slots < 1 || p.n_entries < 1 || p.H > RWKV7_MX_MAX_DIM / p.L)
+        return mx_fail(err_msg, RWKV7_EINVAL, "layers, heads, slots and entries must be >= 1");
+    if (n < 0 || n > RWKV7_STATES_MAX_PAIRS)
+        return mx_fail(err_msg, RWKV7_EINVAL, "n=%lld is outside 0 .. %lld pairs a call", n, RWKV7_STATES_MAX_PAIRS);
+    if (format != RWKV7_MXFP4 && format != RWKV7_MXINT8) return mx_fail(err_msg, RWKV7_EINVAL, "unknown format %lld", format);
+    if (n == 0) return RWKV7_OK;
+    if (!p.wkv || !p.att || !p.ffn || !p.slots || !p.entries || !p.cache || !p.err)
+        return mx_fail(err_msg, RWKV7_EINVAL, "null pointer argument");
+    if (((uintptr_t)p.wkv | (uintptr_t)p.att | (uintptr_t)p.ffn | (uintptr_t)p.cache) & 15u)
+        return mx_fail(err_msg, RWKV7_EINVAL, "the states and the cache must be 16-byte aligned");
+    p.entry_bytes = (int64_t)rwkv7_state_entry_bytes(p.L, p.H, format);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.L * p.H), (unsigned)n);
+    cfg.blockDim = dim3(MXS_THREADS);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    const void *fn = format == RWKV7_MXINT8
+                         ? (save ? (const void *)mx_state_kernel<MXINT8, true> : (const void *)mx_state_kernel<MXINT8, false>)
+                         : (save ? (const void *)mx_state_kernel<MXFP4, true> : (const void *)mx_state_kernel<MXFP4, false>);
+    void *args[] = {&p};
+    return mx_done(err_msg, save ? "saving states" : "loading states", cudaLaunchKernelExC(&cfg, fn, args));
+}
+
+}  // namespace
+
+int rk::mx_ctx_states(bool save, const MxCtxStates &c, const char **err_msg) {
+    MxStateParams p;
+    memset(&p, 0, sizeof p);
+    p.wkv = c.wkv, p.att = c.att, p.ffn = c.ffn;
+    p.L = c.L, p.H = c.H, p.n_slots = c.n_slots, p.n_entries = c.n_entries;
+    p.slots = c.slots, p.entries = c.entries;
+    p.cache = c.cache, p.err = c.err;
+    p.occ = c.occ, p.ndraw = c.ndraw, p.V = c.V;
+    return mx_states(save, p, c.n, c.format, c.stream, err_msg);
+}
+
+extern "C" {
+
+size_t rwkv7_mx4_bytes(int64_t rows, int64_t cols) {
+    if (!mx_size_ok(rows, cols)) return 0;
+    return (size_t)((rows + MX_TILE_M - 1) / MX_TILE_M) * (size_t)((cols + MX_TILE_K - 1) / MX_TILE_K) * MX_TILE_BYTES;
+}
+
+int rwkv7_mx4_quantize(const void *d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, void *d_mx,
+                       void *cuda_stream, const char **err_msg) {
+    MxRowsParams p;
+    int rc = mx_rows_check(p, d_x, dtype, rows, cols, ld, d_mx, err_msg);
+    if (rc || rows == 0) return rc;
+    return mx_done(err_msg, "quantising", mx_launch_rows(mx_quantize_fn(dtype), p, LaunchCfg{static_cast<cudaStream_t>(cuda_stream), false}));
+}
+
+int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y, int32_t dtype, int64_t ld,
+                         void *cuda_stream, const char **err_msg) {
+    MxRowsParams p;
+    int rc = mx_rows_check(p, d_y, dtype, rows, cols, ld, d_mx, err_msg);
+    if (rc || rows == 0) return rc;
+    return mx_done(err_msg, "reading back", mx_launch_rows(mx_dequantize_fn(dtype), p, LaunchCfg{static_cast<cudaStream_t>(cuda_stream), false}));
+}
+
+int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx, int64_t B, const void *d_w_mx, int64_t N,
+                     int64_t K, void *d_y, int32_t y_dtype, int64_t ldy, int32_t activation, uint32_t *d_err,
+                     void *cuda_stream, const char **err_msg) {
+    if (err_msg) *err_msg = "";
+    if (!mx_size_ok(B, K) || !mx_size_ok(N, K) || N < 1)
+        return mx_fail(err_msg, RWKV7_EINVAL, "B must be >= 0, N and K >= 1, all at most 2^24 (N=%lld, K=%lld)", N, K);
+    if (y_dtype < RWKV7_F32 || y_dtype > RWKV7_BF16) return mx_fail(err_msg, RWKV7_EINVAL, "unknown output dtype %lld", y_dtype);
+    if (activation != RWKV7_ACT_NONE && activation != RWKV7_ACT_RELU2)
+        return mx_fail(err_msg, RWKV7_EINVAL, "unknown activation %lld", activation);
+    if (B > 1 && ldy < N) return mx_fail(err_msg, RWKV7_EINVAL, "output row stride %lld is below N=%lld", ldy, N);
+    if (B == 0) return RWKV7_OK;
+    if (!d_x_mx || !d_w_mx || !d_y || !d_err) return mx_fail(err_msg, RWKV7_EINVAL, "null pointer argument");
+    if ((uintptr_t)d_y % (y_dtype == RWKV7_F32 ? 4 : 2))
+        return mx_fail(err_msg, RWKV7_EINVAL, "the output pointer is not aligned to its type");
+    if (((uintptr_t)d_x_mx | (uintptr_t)d_w_mx) & 15u)
+        return mx_fail(err_msg, RWKV7_EINVAL, "MXFP4 matrices must be 16-byte aligned");
+    const LaunchCfg lc{static_cast<cudaStream_t>(cuda_stream), false};
+    if (d_x) {
+        MxRowsParams q;
+        int rc = mx_rows_check(q, d_x, x_dtype, B, K, ldx, d_x_mx, err_msg);
+        if (rc) return rc;
+        rc = mx_done(err_msg, "quantising", mx_launch_rows(mx_quantize_fn(x_dtype), q, lc));
+        if (rc) return rc;
+    }
+    MxLinearParams p;
+    p.x = static_cast<const uint8_t *>(d_x_mx);
+    p.w = static_cast<const uint8_t *>(d_w_mx);
+    p.y = d_y;
+    p.ldy = ldy;
+    p.B = (int)B, p.N = (int)N, p.K = (int)K;
+    p.act = activation;
+    p.err = d_err;
+    cudaError_t e = cudaSuccess;
+    launch_mx_linear(p, y_dtype, lc, &e);
+    return mx_done(err_msg, "MXFP4 product", e);
+}
+
+size_t rwkv7_state_entry_bytes(int32_t n_layer, int32_t n_head, int32_t format) {
+    if (n_layer < 1 || n_head < 1 || n_head > RWKV7_MX_MAX_DIM / n_layer) return 0;
+    if (format != RWKV7_MXFP4 && format != RWKV7_MXINT8) return 0;
+    const int64_t heads = (int64_t)n_layer * n_head;
+    return (size_t)(mx_codes(heads, format) + heads * (MX_HEAD / MX_BLOCK) + heads * 2 * HS * 4);
+}
+
+int rwkv7_states_save(const float *d_wkv, const float *d_shift_att, const float *d_shift_ffn, int32_t n_layer,
+                      int32_t n_head, int32_t n_slots, const int32_t *d_slots, const int32_t *d_entries, int32_t n,
+                      void *d_cache, int32_t n_entries, int32_t format, uint32_t *d_err, void *cuda_stream,
+                      const char **err_msg) {
+    MxStateParams p;
+    memset(&p, 0, sizeof p);
+    p.wkv = const_cast<float *>(d_wkv), p.att = const_cast<float *>(d_shift_att), p.ffn = const_cast<float *>(d_shift_ffn);
+    p.L = n_layer, p.H = n_head, p.n_slots = n_slots, p.n_entries = n_entries;
+    p.slots = d_slots, p.entries = d_entries;
+    p.cache = static_cast<uint8_t *>(d_cache), p.err = d_err;
+    return mx_states(true, p, n, format, cuda_stream, err_msg);
+}
+
+int rwkv7_states_load(float *d_wkv, float *d_shift_att, float *d_shift_ffn, int32_t n_layer, int32_t n_head,
+                      int32_t n_slots, const int32_t *d_slots, const int32_t *d_entries, int32_t n, const void *d_cache,
+                      int32_t n_entries, int32_t format, uint32_t *d_err, void *cuda_stream, const char **err_msg) {
+    MxStateParams p;
+    memset(&p, 0, sizeof p);
+    p.wkv = d_wkv, p.att = d_shift_att, p.ffn = d_shift_ffn;
+    p.L = n_layer, p.H = n_head, p.n_slots = n_slots, p.n_entries = n_entries;
+    p.slots = d_slots, p.entries = d_entries;
+    p.cache = static_cast<uint8_t *>(const_cast<void *>(d_cache)), p.err = d_err;
+    return mx_states(false, p, n, format, cuda_stream, err_msg);
+}
+
+}  // extern "C"

@@ -25,7 +25,7 @@
 #include <vector>
 
 #include "../../include/rwkv7.h"
-#include "internal.cuh"
+#include "mx.cuh"
 
 using namespace rk;
 
@@ -1427,6 +1427,34 @@ int rwkv7_slot_copy(rwkv7_ctx *c, int32_t src, int32_t dst) {
     if (!SLOT_OK(src) || !SLOT_OK(dst)) return fail(c, RWKV7_EINVAL, "slot out of range");
     if (src == dst) return RWKV7_OK;
     return slot_op(c, 1, src, dst);
+}
+
+static int slots_mx(rwkv7_ctx *c, bool save, const int32_t *d_slots, const int32_t *d_entries, int32_t n, void *d_cache,
+                    int32_t n_entries, int32_t format) {
+    MxCtxStates s;
+    memset(&s, 0, sizeof s);
+    s.wkv = c->wkv, s.att = c->shift_att, s.ffn = c->shift_ffn;
+    s.L = c->L, s.H = c->H, s.n_slots = c->n_slots, s.n_entries = n_entries, s.n = n, s.format = format;
+    s.slots = d_slots, s.entries = d_entries;
+    s.cache = (uint8_t *)d_cache;
+    s.err = c->errw;
+    s.occ = c->occ, s.ndraw = c->ndraw, s.V = c->V;
+    s.stream = c->stream;
+    const char *msg = "";
+    const int rc = mx_ctx_states(save, s, &msg);
+    return rc ? fail(c, rc, "%s", msg) : RWKV7_OK;
+}
+
+int rwkv7_slots_save(rwkv7_ctx *c, const int32_t *d_slots, const int32_t *d_entries, int32_t n, void *d_cache,
+                     int32_t n_entries, int32_t format) {
+    if (!c) return RWKV7_EINVAL;
+    return slots_mx(c, true, d_slots, d_entries, n, d_cache, n_entries, format);
+}
+
+int rwkv7_slots_load(rwkv7_ctx *c, const int32_t *d_slots, const int32_t *d_entries, int32_t n, const void *d_cache,
+                     int32_t n_entries, int32_t format) {
+    if (!c) return RWKV7_EINVAL;
+    return slots_mx(c, false, d_slots, d_entries, n, const_cast<void *>(d_cache), n_entries, format);
 }
 
 int rwkv7_slot_set_sampling(rwkv7_ctx *c, int32_t slot, const rwkv7_sampling *sp) {

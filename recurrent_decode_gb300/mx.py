@@ -1,0 +1,216 @@
+"""Microscaled formats of librwkv7 (include/rwkv7.h): MXFP4 matrices and their
+product, and a cache of slot states in MXINT8 or MXFP4.
+
+Argument marshalling only.  Calls run on the current stream of the device their
+tensors are on, allocate outputs and workspaces from torch's allocator on that
+stream, and do not synchronise.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import EINVAL, ETIMEOUT, RWKV7Error, load_library
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_FORMATS = {"mxfp4": 0, "mxint8": 1}
+_ACTIVATIONS = {None: 0, "none": 0, "relu2": 1}
+
+_err: dict[int, torch.Tensor] = {}  # per device: the word in which kernels latch errors
+
+
+def _err_word(dev: torch.device) -> torch.Tensor:
+    w = _err.get(dev.index)
+    if w is None:
+        w = torch.zeros(1, dtype=torch.int32, device=dev)
+        torch.cuda.current_stream(dev).synchronize()  # other streams will use it
+        _err[dev.index] = w
+    return w
+
+
+def _call(fn, dev: torch.device, *args):
+    """fn(*args, stream, &message) with `dev` current."""
+    msg = C.c_char_p()
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, stream, C.byref(msg))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream, C.byref(msg))
+    if rc:
+        raise RWKV7Error(rc, (msg.value or b"").decode())
+
+
+def _rows(x, what: str):
+    """The row stride of a 2-D CUDA tensor whose rows are contiguous."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _DTYPES:
+        raise TypeError(f"{what} must be a CUDA tensor of float32, float16 or bfloat16")
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be two-dimensional, got {x.dim()} dimensions")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"the rows of {what} must be contiguous (stride 1 along the last dimension)")
+    ld = x.stride(0) if rows > 1 else cols
+    if rows > 1 and ld < cols:
+        raise ValueError(f"the rows of {what} overlap (row stride {ld} < {cols})")
+    return ld
+
+
+class MX4Matrix:
+    """An MXFP4 matrix [rows, cols] on the device, in the tile order the product
+    reads (rwkv7_mx4_bytes)."""
+
+    __slots__ = ("data", "rows", "cols")
+
+    def __init__(self, data: torch.Tensor, rows: int, cols: int):
+        self.data, self.rows, self.cols = data, rows, cols
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+    def dequantize(self, dtype=torch.float32, out=None):
+        """The values it stands for (rwkv7_mx4_dequantize)."""
+        if out is None:
+            if dtype not in _DTYPES:
+                raise TypeError("dtype must be float32, float16 or bfloat16")
+            out = torch.empty(self.rows, self.cols, dtype=dtype, device=self.data.device)
+        ld = _rows(out, "out")
+        if out.shape != (self.rows, self.cols) or out.device != self.data.device:
+            raise ValueError("out must have the matrix's shape and device")
+        _call(load_library().rwkv7_mx4_dequantize, out.device, self.data.data_ptr(), self.rows, self.cols, out.data_ptr(),
+              _DTYPES[out.dtype], ld)
+        return out
+
+
+def mx4_empty(rows: int, cols: int, device) -> MX4Matrix:
+    """An MXFP4 matrix whose values are not set yet."""
+    n = load_library().rwkv7_mx4_bytes(rows, cols)
+    if n == 0 and rows != 0 or cols < 1:
+        raise RWKV7Error(EINVAL, f"no MXFP4 matrix of {rows} rows and {cols} columns")
+    return MX4Matrix(torch.empty(n, dtype=torch.uint8, device=device), rows, cols)
+
+
+def mx4_quantize(x, out: MX4Matrix | None = None) -> MX4Matrix:
+    """Rows of x [rows, cols] to MXFP4 (rwkv7_mx4_quantize).  x may be a view with
+    any row stride."""
+    ld = _rows(x, "x")
+    rows, cols = x.shape
+    if out is None:
+        out = mx4_empty(rows, cols, x.device)
+    elif out.shape != (rows, cols) or out.data.device != x.device:
+        raise ValueError("out must have x's shape and device")
+    _call(load_library().rwkv7_mx4_quantize, x.device, x.data_ptr(), _DTYPES[x.dtype], rows, cols, ld, out.data.data_ptr())
+    return out
+
+
+def mx4_linear(x, w: MX4Matrix, out=None, out_dtype=None, activation=None):
+    """act(q(x) w^T): x [B, K] (float32, float16, bfloat16, any row stride; quantised
+    on the way) or an MX4Matrix [B, K], w an MX4Matrix [N, K]; fp32 sums, the
+    result [B, N] rounded once to out's type, or out_dtype (default: x's, float32
+    for an MX4Matrix).  activation: None or "relu2" (max(y, 0)^2).
+    rwkv7_mx4_linear."""
+    if not isinstance(w, MX4Matrix):
+        raise TypeError("w must be an MX4Matrix")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    dev = w.data.device
+    if isinstance(x, MX4Matrix):
+        xq, src, dtype, ldx = x, None, 0, 0
+        x_dev, default = x.data.device, torch.float32
+    else:
+        ldx = _rows(x, "x")
+        src, dtype = x.data_ptr(), _DTYPES[x.dtype]
+        x_dev, default = x.device, x.dtype
+        xq = mx4_empty(x.shape[0], x.shape[1], x_dev)
+    B, K = xq.rows, xq.cols
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, w {w.cols}")
+    if x_dev != dev:
+        raise ValueError(f"x is on {x_dev}, w on {dev}")
+    if out is None:
+        out_dtype = out_dtype or default
+        if out_dtype not in _DTYPES:
+            raise TypeError("out_dtype must be float32, float16 or bfloat16")
+        out = torch.empty(B, w.rows, dtype=out_dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    ldy = _rows(out, "out")
+    if out.shape != (B, w.rows) or out.device != dev:
+        raise ValueError(f"out must be [{B}, {w.rows}] on {dev}")
+    _call(load_library().rwkv7_mx4_linear, dev, src, dtype, ldx, xq.data.data_ptr(), B, w.data.data_ptr(), w.rows, K,
+          out.data_ptr(), _DTYPES[out.dtype], ldy, _ACTIVATIONS[activation], _err_word(dev).data_ptr())
+    return out
+
+
+def mx4_check(device=None):
+    """Wait for the device's current stream and raise if a product's bounded wait
+    gave up since the last check (its output is then undefined)."""
+    dev = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index or 0)
+    w = _err_word(dev)
+    flags = int(w.item())
+    if flags:
+        w.zero_()
+        raise RWKV7Error(ETIMEOUT, f"a bounded wait inside an MXFP4 product gave up (flags 0x{flags:x})")
+
+
+def _pair_count(slots, entries, dev):
+    for what, t in (("slots", slots), ("entries", entries)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise TypeError(f"{what} must be a contiguous int32 tensor on {dev}")
+    if slots.numel() != entries.numel():
+        raise ValueError("slots and entries differ in length")
+    return slots.numel()
+
+
+class StateCache:
+    """Slot states kept in a quarter (MXINT8) or an eighth (MXFP4) of their size:
+    n_entries entries for states of n_layer x n_head heads.  Rwkv7.slots_save and
+    slots_load move a ctx's slots; save and load a pool the caller owns.
+
+    MXINT8 keeps every value to within 1/128 of the largest of its 32 neighbours
+    along a state row, MXFP4 to within 1/6; token-shift states are kept exactly."""
+
+    def __init__(self, n_layer: int, n_head: int, n_entries: int, format: str = "mxint8", device=None):
+        if format not in _FORMATS:
+            raise ValueError(f"unknown format {format!r}: mxint8 or mxfp4")
+        self.n_layer, self.n_head, self.n_entries = int(n_layer), int(n_head), int(n_entries)
+        self.format = _FORMATS[format]
+        self.entry_bytes = load_library().rwkv7_state_entry_bytes(self.n_layer, self.n_head, self.format)
+        if self.entry_bytes == 0 or self.n_entries < 1:
+            raise RWKV7Error(EINVAL, "layers, heads and entries must be >= 1")
+        dev = torch.device("cuda" if device is None else device)
+        self.data = torch.empty(self.n_entries * self.entry_bytes, dtype=torch.uint8, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.data.device)
+
+    def _states(self, fn, states, slots, entries):
+        wkv, att, ffn = states
+        dev, L, H = self.data.device, self.n_layer, self.n_head
+        for what, t in (("wkv", wkv), ("shift_att", att), ("shift_ffn", ffn)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_contiguous() or t.device != dev:
+                raise TypeError(f"{what} must be a contiguous float32 tensor on {dev}")
+        if wkv.dim() != 5 or att.dim() != 3:
+            raise ValueError("states are wkv [L, slots, H, 64, 64] and two token shifts [L, slots, 64 H]")
+        n_slots = wkv.shape[1]
+        if wkv.shape != (L, n_slots, H, 64, 64) or att.shape != (L, n_slots, 64 * H) or ffn.shape != att.shape:
+            raise ValueError(f"states must be wkv [{L}, slots, {H}, 64, 64] and two token shifts [{L}, slots, {64 * H}]")
+        n = _pair_count(slots, entries, dev)
+        _call(fn, dev, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
+              entries.data_ptr(), n, self.data.data_ptr(), self.n_entries, self.format, self.err.data_ptr())
+
+    def save(self, states, slots, entries):
+        """Keep the states of `slots` in `entries` (rwkv7_states_save).  states:
+        (wkv [L, n_slots, H, 64, 64], shift_att, shift_ffn [L, n_slots, 64 H])."""
+        self._states(load_library().rwkv7_states_save, states, slots, entries)
+
+    def load(self, states, entries, slots):
+        """Put the kept states of `entries` into `slots` (rwkv7_states_load)."""
+        self._states(load_library().rwkv7_states_load, states, slots, entries)
+
+    def check(self):
+        """Wait for the stream and raise if a save or load had a bad or repeated index."""
+        flags = int(self.err.item())
+        if flags:
+            self.err.zero_()
+            raise RWKV7Error(EINVAL, "slot or entry out of range, or written twice in one call (flags 0x%x)" % flags)
