@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_quantize_kernel(const MxRowsP
     using E = typename MxElem<T>::type;
     const int64_t line = (int64_t)blockIdx.x * (MXQ_THREADS / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    pdl_launch();  // a product of these rows may start fetching its weights
     if (line >= p.rows * p.kt) return;
     const int64_t r = line / p.kt, t = line % p.kt;
     const int64_t c0 = t * MX_TILE_K + lane * 8;
@@ -367,7 +368,7 @@ int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx
     p.act = activation;
     p.err = d_err;
     cudaError_t e = cudaSuccess;
-    launch_mx_linear(p, y_dtype, lc, &e);
+    launch_mx_linear(p, y_dtype, LaunchCfg{lc.stream, d_x != nullptr}, &e);
     return mx_done(err_msg, "MXFP4 product", e);
 }
 
