@@ -397,7 +397,7 @@ RWKV7_API size_t rwkv7_state_entry_bytes(int32_t n_layer, int32_t n_head, int32_
  * pair i is slot d_slots[i] and entry d_entries[i] (device int32 [n],
  * 0 <= n <= RWKV7_STATES_MAX_PAIRS).  The pool is fp32, as the ctx keeps it: d_wkv
  * [n_layer][n_slots][n_head][64][64], d_shift_att and d_shift_ffn
- * [n_layer][n_slots][64 * n_head], 16-byte aligned.  The wkv states are quantised
+ * [n_layer][n_slots][64 * n_head], 16-byte aligned (d_wkv 32).  The wkv states are quantised
  * along their rows (the key channels), the shift states kept exactly.  Several
  * pairs may read the same slot or entry.  Where two pairs write the same one the
  * first is carried out, the others are not, and bit 4 is set in *d_err (a device

@@ -35,72 +35,149 @@ struct MxElem<MX_BF16> {
 
 struct MxRowsParams {
     void *x;  // [rows] at ld
-    int64_t rows, cols, ld;
+    int64_t cols, ld;
     uint8_t *mx;
-    int64_t kt;  // column tiles
-    int vec;     // rows start on 16-byte boundaries
+    int lines, kt;  // lines (rows x column tiles), column tiles
+    int per;        // consecutive lines a warp takes
+    int vec;        // the lanes' eight values start on 16-byte (fp32: 32-byte) boundaries in every row
 };
 
 constexpr int MXQ_THREADS = 256;
+constexpr int MXQ_LINES = 4;  // lines of a warp at most, their loads issued together
+constexpr int MXQ_MANY = 152 * 8 * 8;  // from here on (eight warps on each SM eight times over) a warp takes them all
 
-// One warp per (row, column tile): eight values a lane.
+// Where lane's eight values of a line lie in its tile.
+__device__ __forceinline__ int64_t mx_tile_at(int r, int t, int kt) {
+    return ((int64_t)(r / MX_TILE_M) * kt + t) * MX_TILE_BYTES;
+}
+__device__ __forceinline__ int mx_code_at(int rr, int lane) {
+    return (int)MX_SCALE_BYTES + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4;
+}
+__device__ __forceinline__ int mx_power_at(int rr, int blk) {
+    return (blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4 + (blk & 3);
+}
+
+// A warp takes p.per consecutive lines (a line: 256 columns of a row), eight values a
+// lane.  Rows off the 16-byte grid are read value by value, neighbours by
+// neighbouring lanes, and turned through shared memory.
 template <int T>
 __global__ void __launch_bounds__(MXQ_THREADS) mx4_quantize_kernel(const MxRowsParams p) {
     using E = typename MxElem<T>::type;
-    const int64_t line = (int64_t)blockIdx.x * (MXQ_THREADS / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    __shared__ float turn[MXQ_THREADS / 32][MX_TILE_K];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = (blockIdx.x * (MXQ_THREADS / 32) + warp) * p.per;
     pdl_launch();  // a product of these rows may start fetching its weights
-    if (line >= p.rows * p.kt) return;
-    const int64_t r = line / p.kt, t = line % p.kt;
-    const int64_t c0 = t * MX_TILE_K + lane * 8;
-    const E *src = (const E *)p.x + r * p.ld + c0;
-    float v[8];
-    if (p.vec && c0 + 8 <= p.cols) {
-        alignas(16) E u[8];
+    const int n = min(p.per, p.lines - first);
+    if (n <= 0) return;
+    const int r0 = first / p.kt, t0 = first - r0 * p.kt;
+    float v[MXQ_LINES][8];
+    int r = r0, t = t0;
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(u) / 16; ++i) ((uint4 *)u)[i] = ((const uint4 *)src)[i];
+    for (int l = 0; l < MXQ_LINES; ++l) {
+        if (l >= n) break;
+        const int64_t c0 = (int64_t)t * MX_TILE_K;
+        const E *src = (const E *)p.x + r * p.ld + c0;
+        if (p.vec && c0 + lane * 8 + 8 <= p.cols) {
+            if constexpr (T == MX_F32) {
+                ld_v8(v[l], src + lane * 8);
+            } else {
+                alignas(16) E u[8];
+                *(uint4 *)u = *(const uint4 *)(src + lane * 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = MxElem<T>::up(u[i]);
-    } else {
+                for (int i = 0; i < 8; ++i) v[l][i] = MxElem<T>::up(u[i]);
+            }
+        } else if (p.vec) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c0 + i < p.cols ? MxElem<T>::up(src[i]) : 0.0f;
+            for (int i = 0; i < 8; ++i)
+                v[l][i] = c0 + lane * 8 + i < p.cols ? MxElem<T>::up(src[lane * 8 + i]) : 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[l][i] = c0 + i * 32 + lane < p.cols ? MxElem<T>::up(src[i * 32 + lane]) : 0.0f;
+        }
+        if (++t == p.kt) t = 0, ++r;
     }
-    const uint32_t s = mx_scale<MXFP4>(mx_quad_top(v));
-    const float f = s == 255u ? 0.0f : mx_inverse(s);
+    r = r0, t = t0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = s == 255u ? 0.0f : v[i] * f;
-    uint8_t *tile = p.mx + ((r / MX_TILE_M) * p.kt + t) * MX_TILE_BYTES;
-    const int rr = (int)(r % MX_TILE_M), blk = lane >> 2;
-    *(uint32_t *)(tile + MX_SCALE_BYTES + rr * 128 + ((blk ^ (rr & 7)) << 4) + (lane & 3) * 4) = fp4_pack8(v);
-    if ((lane & 3) == 0) tile[(blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4 + (blk & 3)] = (uint8_t)s;
+    for (int l = 0; l < MXQ_LINES; ++l) {
+        if (l >= n) break;
+        if (!p.vec) {
+            float *tw = turn[warp];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tw[i * 32 + lane] = v[l][i];
+            __syncwarp();
+            *(float4 *)&v[l][0] = *(const float4 *)&tw[lane * 8];
+            *(float4 *)&v[l][4] = *(const float4 *)&tw[lane * 8 + 4];
+        }
+        const uint32_t s = mx_scale<MXFP4>(mx_quad_top(v[l]));
+        const float f = mx_inverse(s);  // a block without a number: its codes do not matter
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[l][i] *= f;
+        // the powers of four blocks to one word, held by lanes 0 and 16
+        uint32_t w = s | __shfl_down_sync(0xffffffffu, s, 4) << 8;
+        w |= __shfl_down_sync(0xffffffffu, w, 8) << 16;
+        uint8_t *tile = p.mx + mx_tile_at(r, t, p.kt);
+        const int rr = r % MX_TILE_M;
+        *(uint32_t *)(tile + mx_code_at(rr, lane)) = fp4_pack8(v[l]);
+        if ((lane & 15) == 0) *(uint32_t *)(tile + mx_power_at(rr, lane >> 2)) = w;
+        if (++t == p.kt) t = 0, ++r;
+    }
 }
 
 template <int T>
 __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRowsParams p) {
     using E = typename MxElem<T>::type;
-    const int64_t line = (int64_t)blockIdx.x * (MXQ_THREADS / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (line >= p.rows * p.kt) return;
-    const int64_t r = line / p.kt, t = line % p.kt;
-    const int64_t c0 = t * MX_TILE_K + lane * 8;
-    const uint8_t *tile = p.mx + ((r / MX_TILE_M) * p.kt + t) * MX_TILE_BYTES;
-    const int rr = (int)(r % MX_TILE_M), blk = lane >> 2;
-    const uint32_t code = *(const uint32_t *)(tile + MX_SCALE_BYTES + rr * 128 + ((blk ^ (rr & 7)) << 4) + (lane & 3) * 4);
-    const uint32_t s = tile[(blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4 + (blk & 3)];
-    float v[8];
-    fp4_unpack8(code, v);
-    const float f = s == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s);
-    alignas(16) E u[8];
+    __shared__ float turn[MXQ_THREADS / 32][MX_TILE_K];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = (blockIdx.x * (MXQ_THREADS / 32) + warp) * p.per;
+    const int n = min(p.per, p.lines - first);
+    if (n <= 0) return;
+    const int r0 = first / p.kt, t0 = first - r0 * p.kt;
+    uint32_t code[MXQ_LINES], s[MXQ_LINES];
+    int r = r0, t = t0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = MxElem<T>::down(v[i] * f);
-    E *dst = (E *)p.x + r * p.ld + c0;
-    if (p.vec && c0 + 8 <= p.cols) {
+    for (int l = 0; l < MXQ_LINES; ++l) {
+        if (l >= n) break;
+        const uint8_t *tile = p.mx + mx_tile_at(r, t, p.kt);
+        code[l] = *(const uint32_t *)(tile + mx_code_at(r % MX_TILE_M, lane));
+        s[l] = tile[mx_power_at(r % MX_TILE_M, lane >> 2)];
+        if (++t == p.kt) t = 0, ++r;
+    }
+    r = r0, t = t0;
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(u) / 16; ++i) ((uint4 *)dst)[i] = ((const uint4 *)u)[i];
-    } else {
+    for (int l = 0; l < MXQ_LINES; ++l) {
+        if (l >= n) break;
+        float v[8];
+        fp4_unpack8(code[l], v);
+        const float f = s[l] == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s[l]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c0 + i < p.cols) dst[i] = u[i];
+        for (int i = 0; i < 8; ++i) v[i] *= f;
+        const int64_t c0 = (int64_t)t * MX_TILE_K;
+        E *dst = (E *)p.x + r * p.ld + c0;
+        if (p.vec && c0 + lane * 8 + 8 <= p.cols) {
+            if constexpr (T == MX_F32) {
+                st_v8(dst + lane * 8, v);
+            } else {
+                alignas(16) E u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = MxElem<T>::down(v[i]);
+                *(uint4 *)(dst + lane * 8) = *(const uint4 *)u;
+            }
+        } else if (p.vec) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + lane * 8 + i < p.cols) dst[lane * 8 + i] = MxElem<T>::down(v[i]);
+        } else {
+            float *tw = turn[warp];
+            __syncwarp();
+            *(float4 *)&tw[lane * 8] = *(const float4 *)&v[0];
+            *(float4 *)&tw[lane * 8 + 4] = *(const float4 *)&v[4];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + i * 32 + lane < p.cols) dst[i * 32 + lane] = MxElem<T>::down(tw[i * 32 + lane]);
+        }
+        if (++t == p.kt) t = 0, ++r;
     }
 }
 
@@ -112,6 +189,7 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRow
 // ---------------------------------------------------------------------------
 constexpr int MXS_THREADS = 256;
 constexpr int MX_HEAD = HS * HS;  // values of one head's state
+constexpr int MXS_GROUPS = MX_HEAD / 8 / MXS_THREADS;  // groups of eight values a thread takes
 
 struct MxStateParams {
     float *wkv, *att, *ffn;  // [L][n_slots][H][64][64], [L][n_slots][d] twice
@@ -169,43 +247,54 @@ __global__ void __launch_bounds__(MXS_THREADS) mx_state_kernel(const MxStatePara
         for (int64_t k = a + threadIdx.x; k < b; k += MXS_THREADS) p.occ[(int64_t)slot * p.V + k] = 0.0f;
         if (hl == 0 && threadIdx.x == 0) p.ndraw[slot] = 0ull;
     }
+    if constexpr (SAVE) {
+        float v[MXS_GROUPS][8];
 #pragma unroll
-    for (int g = threadIdx.x; g < MX_HEAD / 8; g += MXS_THREADS) {
-        float v[8];
-        if (SAVE) {
-            *(float4 *)&v[0] = ((const float4 *)st)[2 * g];
-            *(float4 *)&v[4] = ((const float4 *)st)[2 * g + 1];
-            const uint32_t s = mx_scale<FMT>(mx_quad_top(v));
-            const float f = s == 255u ? 0.0f : mx_inverse(s);
+        for (int i = 0; i < MXS_GROUPS; ++i) ld_v8(v[i], st + (threadIdx.x + i * MXS_THREADS) * 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = s == 255u ? 0.0f : v[j] * f;
-            if (FMT == MXFP4) {
-                ((uint32_t *)codes)[g] = fp4_pack8(v);
+        for (int i = 0; i < MXS_GROUPS; ++i) {
+            const int g = threadIdx.x + i * MXS_THREADS;
+            const uint32_t s = mx_scale<FMT>(mx_quad_top(v[i]));
+            const float f = mx_inverse(s);  // a block without a number: its codes do not matter
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] *= f;
+            if constexpr (FMT == MXFP4) {
+                ((uint32_t *)codes)[g] = fp4_pack8(v[i]);
             } else {
                 uint32_t w[2] = {0, 0};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int q = min(127, max(-127, __float2int_rn(v[j] * 64.0f)));
+                    const int q = min(127, max(-127, __float2int_rn(v[i][j] * 64.0f)));
                     w[j >> 2] |= ((uint32_t)q & 255u) << (8 * (j & 3));
                 }
                 ((uint2 *)codes)[g] = make_uint2(w[0], w[1]);
             }
             if ((g & 3) == 0) scales[g >> 2] = (uint8_t)s;
-        } else {
-            const uint32_t s = scales[g >> 2];
-            const float f = s == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s);
-            if (FMT == MXFP4) {
-                fp4_unpack8(((const uint32_t *)codes)[g], v);
+        }
+    } else {
+        uint32_t s[MXS_GROUPS];
+        uint2 w[MXS_GROUPS];
+#pragma unroll
+        for (int i = 0; i < MXS_GROUPS; ++i) {
+            const int g = threadIdx.x + i * MXS_THREADS;
+            s[i] = scales[g >> 2];
+            if constexpr (FMT == MXFP4) w[i].x = ((const uint32_t *)codes)[g];
+            else w[i] = ((const uint2 *)codes)[g];
+        }
+#pragma unroll
+        for (int i = 0; i < MXS_GROUPS; ++i) {
+            float v[8];
+            if constexpr (FMT == MXFP4) {
+                fp4_unpack8(w[i].x, v);
             } else {
-                const uint2 w = ((const uint2 *)codes)[g];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * (1.0f / 64.0f);
+                    v[j] = (float)(int8_t)((j < 4 ? w[i].x : w[i].y) >> (8 * (j & 3))) * (1.0f / 64.0f);
             }
+            const float f = s[i] == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= f;
-            ((float4 *)st)[2 * g] = *(float4 *)&v[0];
-            ((float4 *)st)[2 * g + 1] = *(float4 *)&v[4];
+            st_v8(st + (threadIdx.x + i * MXS_THREADS) * 8, v);
         }
     }
 }
@@ -246,19 +335,22 @@ int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, i
     if ((uintptr_t)x % size) return mx_fail(err_msg, RWKV7_EINVAL, "the rows' pointer is not aligned to its type");
     if ((uintptr_t)mx & 15u) return mx_fail(err_msg, RWKV7_EINVAL, "the MXFP4 matrix must be 16-byte aligned");
     p.x = const_cast<void *>(x);
-    p.rows = rows;
     p.cols = cols;
     p.ld = ld;
     p.mx = static_cast<uint8_t *>(const_cast<void *>(mx));
-    p.kt = (cols + MX_TILE_K - 1) / MX_TILE_K;
-    p.vec = (uintptr_t)x % 16 == 0 && (rows <= 1 || ld * size % 16 == 0);
+    p.kt = (int)((cols + MX_TILE_K - 1) / MX_TILE_K);
+    if (rows > (INT32_MAX - 4096) / p.kt) return mx_fail(err_msg, RWKV7_EINVAL, "%lld rows of %lld columns are too many", rows, cols);
+    p.lines = (int)(rows * p.kt);
+    const int step = 8 * size;  // bytes of a lane's eight values
+    p.vec = (uintptr_t)x % step == 0 && (rows <= 1 || ld * size % step == 0);
     return RWKV7_OK;
 }
 
 cudaError_t mx_launch_rows(const void *kernel, MxRowsParams &p, const LaunchCfg &lc) {
-    const int64_t lines = p.rows * p.kt, per = MXQ_THREADS / 32;
+    p.per = p.lines >= MXQ_MANY ? MXQ_LINES : 1;
+    const int per = MXQ_THREADS / 32 * p.per;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((lines + per - 1) / per));
+    cfg.gridDim = dim3((unsigned)((p.lines + (int64_t)per - 1) / per));
     cfg.blockDim = dim3(MXQ_THREADS);
     cfg.stream = lc.stream;
     void *args[] = {&p};
@@ -285,8 +377,8 @@ int mx_states(bool save, MxStateParams &p, int32_t n, int32_t format, void *stre
     if (n == 0) return RWKV7_OK;
     if (!p.wkv || !p.att || !p.ffn || !p.slots || !p.entries || !p.cache || !p.err)
         return mx_fail(err_msg, RWKV7_EINVAL, "null pointer argument");
-    if (((uintptr_t)p.wkv | (uintptr_t)p.att | (uintptr_t)p.ffn | (uintptr_t)p.cache) & 15u)
-        return mx_fail(err_msg, RWKV7_EINVAL, "the states and the cache must be 16-byte aligned");
+    if (((uintptr_t)p.wkv & 31u) || (((uintptr_t)p.att | (uintptr_t)p.ffn | (uintptr_t)p.cache) & 15u))
+        return mx_fail(err_msg, RWKV7_EINVAL, "wkv must be 32-byte aligned, the shift states and the cache 16-byte aligned");
     p.entry_bytes = (int64_t)rwkv7_state_entry_bytes(p.L, p.H, format);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.L * p.H), (unsigned)n);

@@ -16,45 +16,60 @@ from . import EINVAL, ETIMEOUT, RWKV7Error, load_library
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _FORMATS = {"mxfp4": 0, "mxint8": 1}
 _ACTIVATIONS = {None: 0, "none": 0, "relu2": 1}
+_MAX_DIM = 1 << 24  # RWKV7_MX_MAX_DIM
+
+# The handle of a device's current stream and the current device, without the
+# objects that torch.cuda.current_stream builds (2 us a call; a small product takes 5).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 _err: dict[int, torch.Tensor] = {}  # per device: the word in which kernels latch errors
 
 
-def _err_word(dev: torch.device) -> torch.Tensor:
-    w = _err.get(dev.index)
+def _err_word(dev: int) -> torch.Tensor:
+    w = _err.get(dev)
     if w is None:
-        w = torch.zeros(1, dtype=torch.int32, device=dev)
+        w = torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
         torch.cuda.current_stream(dev).synchronize()  # other streams will use it
-        _err[dev.index] = w
+        _err[dev] = w
     return w
 
 
-def _call(fn, dev: torch.device, *args):
-    """fn(*args, stream, &message) with `dev` current."""
+def _call(fn, dev: int, *args):
+    """fn(*args, stream, &message) on the current stream of device `dev`, with it current."""
     msg = C.c_char_p()
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, stream, C.byref(msg))
+    if dev == _current_device():
+        rc = fn(*args, _raw_stream(dev), C.byref(msg))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream, C.byref(msg))
+            rc = fn(*args, _raw_stream(dev), C.byref(msg))
     if rc:
         raise RWKV7Error(rc, (msg.value or b"").decode())
 
 
 def _rows(x, what: str):
-    """The row stride of a 2-D CUDA tensor whose rows are contiguous."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _DTYPES:
+    """(rows, cols, row stride, type code) of a 2-D CUDA tensor whose rows are contiguous."""
+    dtype = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    if dtype is None or not x.is_cuda:
         raise TypeError(f"{what} must be a CUDA tensor of float32, float16 or bfloat16")
     if x.dim() != 2:
         raise ValueError(f"{what} must be two-dimensional, got {x.dim()} dimensions")
     rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    ld, step = x.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"the rows of {what} must be contiguous (stride 1 along the last dimension)")
-    ld = x.stride(0) if rows > 1 else cols
-    if rows > 1 and ld < cols:
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError(f"the rows of {what} overlap (row stride {ld} < {cols})")
-    return ld
+    return rows, cols, ld, dtype
+
+
+def _bytes(rows: int, cols: int) -> int:
+    """rwkv7_mx4_bytes, or a refusal."""
+    if not (0 <= rows <= _MAX_DIM and 1 <= cols <= _MAX_DIM):
+        raise RWKV7Error(EINVAL, f"no MXFP4 matrix of {rows} rows and {cols} columns")
+    return (rows + 127 >> 7) * (cols + 255 >> 8) * 17408
 
 
 class MX4Matrix:
@@ -64,6 +79,10 @@ class MX4Matrix:
     __slots__ = ("data", "rows", "cols")
 
     def __init__(self, data: torch.Tensor, rows: int, cols: int):
+        if not data.is_cuda or data.dtype != torch.uint8 or not data.is_contiguous():
+            raise TypeError("an MXFP4 matrix is a contiguous uint8 tensor on a CUDA device")
+        if data.numel() != _bytes(rows, cols):
+            raise ValueError(f"an MXFP4 matrix of {rows} x {cols} takes {_bytes(rows, cols)} bytes, got {data.numel()}")
         self.data, self.rows, self.cols = data, rows, cols
 
     @property
@@ -76,32 +95,28 @@ class MX4Matrix:
             if dtype not in _DTYPES:
                 raise TypeError("dtype must be float32, float16 or bfloat16")
             out = torch.empty(self.rows, self.cols, dtype=dtype, device=self.data.device)
-        ld = _rows(out, "out")
-        if out.shape != (self.rows, self.cols) or out.device != self.data.device:
+        rows, cols, ld, code = _rows(out, "out")
+        if (rows, cols) != (self.rows, self.cols) or out.get_device() != self.data.get_device():
             raise ValueError("out must have the matrix's shape and device")
-        _call(load_library().rwkv7_mx4_dequantize, out.device, self.data.data_ptr(), self.rows, self.cols, out.data_ptr(),
-              _DTYPES[out.dtype], ld)
+        _call(load_library().rwkv7_mx4_dequantize, out.get_device(), self.data.data_ptr(), rows, cols, out.data_ptr(),
+              code, ld)
         return out
 
 
 def mx4_empty(rows: int, cols: int, device) -> MX4Matrix:
     """An MXFP4 matrix whose values are not set yet."""
-    n = load_library().rwkv7_mx4_bytes(rows, cols)
-    if n == 0 and rows != 0 or cols < 1:
-        raise RWKV7Error(EINVAL, f"no MXFP4 matrix of {rows} rows and {cols} columns")
-    return MX4Matrix(torch.empty(n, dtype=torch.uint8, device=device), rows, cols)
+    return MX4Matrix(torch.empty(_bytes(rows, cols), dtype=torch.uint8, device=device), rows, cols)
 
 
 def mx4_quantize(x, out: MX4Matrix | None = None) -> MX4Matrix:
     """Rows of x [rows, cols] to MXFP4 (rwkv7_mx4_quantize).  x may be a view with
     any row stride."""
-    ld = _rows(x, "x")
-    rows, cols = x.shape
+    rows, cols, ld, code = _rows(x, "x")
     if out is None:
         out = mx4_empty(rows, cols, x.device)
     elif out.shape != (rows, cols) or out.data.device != x.device:
         raise ValueError("out must have x's shape and device")
-    _call(load_library().rwkv7_mx4_quantize, x.device, x.data_ptr(), _DTYPES[x.dtype], rows, cols, ld, out.data.data_ptr())
+    _call(load_library().rwkv7_mx4_quantize, x.get_device(), x.data_ptr(), code, rows, cols, ld, out.data.data_ptr())
     return out
 
 
@@ -115,40 +130,39 @@ def mx4_linear(x, w: MX4Matrix, out=None, out_dtype=None, activation=None):
         raise TypeError("w must be an MX4Matrix")
     if activation not in _ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
-    dev = w.data.device
+    dev = w.data.get_device()
     if isinstance(x, MX4Matrix):
-        xq, src, dtype, ldx = x, None, 0, 0
-        x_dev, default = x.data.device, torch.float32
+        xq, src, code, ldx = x, None, 0, 0
+        B, K, x_dev, default = x.rows, x.cols, x.data.get_device(), torch.float32
     else:
-        ldx = _rows(x, "x")
-        src, dtype = x.data_ptr(), _DTYPES[x.dtype]
-        x_dev, default = x.device, x.dtype
-        xq = mx4_empty(x.shape[0], x.shape[1], x_dev)
-    B, K = xq.rows, xq.cols
+        B, K, ldx, code = _rows(x, "x")
+        src, x_dev, default = x.data_ptr(), x.get_device(), x.dtype
     if K != w.cols:
         raise ValueError(f"x has {K} columns, w {w.cols}")
     if x_dev != dev:
-        raise ValueError(f"x is on {x_dev}, w on {dev}")
+        raise ValueError(f"x is on cuda:{x_dev}, w on cuda:{dev}")
+    if src is not None:
+        xq = mx4_empty(B, K, x.device)
     if out is None:
         out_dtype = out_dtype or default
         if out_dtype not in _DTYPES:
             raise TypeError("out_dtype must be float32, float16 or bfloat16")
-        out = torch.empty(B, w.rows, dtype=out_dtype, device=dev)
+        out = torch.empty(B, w.rows, dtype=out_dtype, device=w.data.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    ldy = _rows(out, "out")
-    if out.shape != (B, w.rows) or out.device != dev:
-        raise ValueError(f"out must be [{B}, {w.rows}] on {dev}")
-    _call(load_library().rwkv7_mx4_linear, dev, src, dtype, ldx, xq.data.data_ptr(), B, w.data.data_ptr(), w.rows, K,
-          out.data_ptr(), _DTYPES[out.dtype], ldy, _ACTIVATIONS[activation], _err_word(dev).data_ptr())
+    rows, cols, ldy, out_code = _rows(out, "out")
+    if rows != B or cols != w.rows or out.get_device() != dev:
+        raise ValueError(f"out must be [{B}, {w.rows}] on cuda:{dev}")
+    _call(load_library().rwkv7_mx4_linear, dev, src, code, ldx, xq.data.data_ptr(), B, w.data.data_ptr(), cols, K,
+          out.data_ptr(), out_code, ldy, _ACTIVATIONS[activation], _err_word(dev).data_ptr())
     return out
 
 
 def mx4_check(device=None):
     """Wait for the device's current stream and raise if a product's bounded wait
     gave up since the last check (its output is then undefined)."""
-    dev = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index or 0)
-    w = _err_word(dev)
+    index = None if device is None else torch.device(device).index
+    w = _err_word(torch.cuda.current_device() if index is None else index)
     flags = int(w.item())
     if flags:
         w.zero_()
@@ -169,8 +183,8 @@ class StateCache:
     n_entries entries for states of n_layer x n_head heads.  Rwkv7.slots_save and
     slots_load move a ctx's slots; save and load a pool the caller owns.
 
-    MXINT8 keeps every value to within 1/128 of the largest of its 32 neighbours
-    along a state row, MXFP4 to within 1/6; token-shift states are kept exactly."""
+    MXINT8 keeps every value to within 1/127 of the largest of its block of 32 along
+    a state row, MXFP4 to within 1/5; token-shift states are kept exactly."""
 
     def __init__(self, n_layer: int, n_head: int, n_entries: int, format: str = "mxint8", device=None):
         if format not in _FORMATS:
@@ -180,8 +194,10 @@ class StateCache:
         self.entry_bytes = load_library().rwkv7_state_entry_bytes(self.n_layer, self.n_head, self.format)
         if self.entry_bytes == 0 or self.n_entries < 1:
             raise RWKV7Error(EINVAL, "layers, heads and entries must be >= 1")
-        dev = torch.device("cuda" if device is None else device)
-        self.data = torch.empty(self.n_entries * self.entry_bytes, dtype=torch.uint8, device=dev)
+        self.data = torch.empty(self.n_entries * self.entry_bytes, dtype=torch.uint8,
+                                device="cuda" if device is None else device)
+        if not self.data.is_cuda:
+            raise TypeError("a state cache lies on a CUDA device")
         self.err = torch.zeros(1, dtype=torch.int32, device=self.data.device)
 
     def _states(self, fn, states, slots, entries):
@@ -196,7 +212,7 @@ class StateCache:
         if wkv.shape != (L, n_slots, H, 64, 64) or att.shape != (L, n_slots, 64 * H) or ffn.shape != att.shape:
             raise ValueError(f"states must be wkv [{L}, slots, {H}, 64, 64] and two token shifts [{L}, slots, {64 * H}]")
         n = _pair_count(slots, entries, dev)
-        _call(fn, dev, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
+        _call(fn, dev.index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
               entries.data_ptr(), n, self.data.data_ptr(), self.n_entries, self.format, self.err.data_ptr())
 
     def save(self, states, slots, entries):
