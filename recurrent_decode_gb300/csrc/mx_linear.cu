@@ -8,16 +8,19 @@
 // weights.  128 weight rows form the M side and the tokens the N side (padded to
 // 16, at most 256), so a decode batch reads each weight once.
 //
-// One CTA computes one tile of 128 outputs x up to 256 tokens over a range of
-// column tiles of 256:
-//   warp 0      bulk copies of whole tiles -- codes and powers as they lie, no
-//               tensor map -- into a ring of stages; the weights of the first
-//               stages are requested before the wait for the kernel that
-//               quantises x
-//   warp 1      per stage: powers from shared into tensor memory (tcgen05.cp, in
-//               order before the products of the same thread), four products
-//   warps 2-9   accumulator -> activation -> y; lane = output, so a warp's store
-//               of one token covers 32 neighbouring outputs
+// A tile is 128 outputs x nt tokens over all of K.  One CTA a SM walks its share of
+// the tiles; where there are fewer tiles than SMs the CTAs of a cluster share one
+// tile's column tiles and add their partial sums through each other's shared memory,
+// in rank order, so a result does not depend on timing.
+//   warp 0       bulk copies of whole tiles of 128 x 256 -- codes and powers as they
+//                lie, no tensor map -- into a ring of stages that runs on across
+//                tiles; the weights of the first stages are requested before the wait
+//                for the kernel that quantises x
+//   warp 1       per stage: powers from shared into tensor memory (tcgen05.cp, in
+//                order before the products of the same thread), four products
+//   warps 2-17   the accumulator to registers, then, while the next tile's products
+//                run, activation and y; lane = output, so a warp's store of one token
+//                covers 32 neighbouring outputs
 // Each stage has columns of its own for its powers: they are overwritten only
 // after the commit that also frees the stage's shared memory.
 #include <algorithm>
@@ -26,19 +29,26 @@
 
 namespace rk {
 
-constexpr int MXL_EPI_WARPS = 8;
-constexpr int MXL_THREADS = 64 + 32 * MXL_EPI_WARPS;
-constexpr int MXL_MAX_STAGES = 8;
-constexpr uint32_t MXL_SMEM_MAX = 227 * 1024 - 256;  // a CTA's dynamic part
+constexpr int MXL_EPI_WARPS = 16;
+constexpr int MXL_EPI_THREADS = 32 * MXL_EPI_WARPS;
+constexpr int MXL_THREADS = 64 + MXL_EPI_THREADS;
+constexpr int MXL_MAX_STAGES = 10;
+constexpr int MXL_MAX_SPLIT = 8;  // CTAs of a portable cluster
+constexpr uint32_t MXL_SMEM_MAX = 226 * 1024;  // a CTA's dynamic part
+constexpr uint32_t MXL_SF = 24;  // tensor memory columns of a stage's powers: 8 of w, 2 x 8 of x
+constexpr int MXL_TOKENS = 256;  // of a tile, at most
+constexpr int MXL_CHUNKS = MXL_TOKENS / 16 / (MXL_EPI_WARPS / 4);  // of 16 tokens, that an epilogue warp holds
 
 struct MxLinearArgs {
     MxLinearParams p;
-    int kt;       // column tiles
-    int nt;       // tokens of a full tile, a multiple of 16
-    int stages;
-    uint32_t xbytes;  // shared memory of a stage's x: both records' powers, then the codes
+    int kt;           // column tiles
+    int nt;           // tokens of a full tile, a multiple of 16
+    int rtiles, tiles;  // tiles of outputs; all tiles, outputs fastest
+    int stages;       // of the ring
+    int split;        // CTAs of a cluster, which share one tile's column tiles
+    int pack;         // y's rows allow stores of two (16-bit types) or four (split) neighbours
+    uint32_t stage_bytes;
     uint32_t ncols;   // tensor memory columns
-    uint32_t sfcol;   // first column of the powers
 };
 
 // Descriptor of 32 rows of 16 bytes, one after another (tcgen05.cp of powers).
@@ -65,31 +75,143 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int N, int half) {
     return 1u << 7 | 1u << 10 | (uint32_t)(N >> 3) << 17 | 1u << 23 | 1u << 27 | (uint32_t)half << 5 | (uint32_t)half << 30;
 }
 
-template <typename O>
-__device__ __forceinline__ O mx_out(float v);
-template <>
-__device__ __forceinline__ float mx_out(float v) { return v; }
-template <>
-__device__ __forceinline__ __half mx_out(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 mx_out(float v) { return __float2bfloat16_rn(v); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+// One stage: its powers into tensor memory, then `ni` products of 64 columns each.
+// XC: tensor memory columns of x's powers for 128 columns of K (4 a record of 128 tokens).
+template <int XC>
+__device__ __forceinline__ void issue_stage(uint32_t tmem, uint32_t sw, uint32_t sx, uint32_t sfa, uint32_t sfb,
+                                            uint32_t id0, uint32_t id1, bool add, int ni) {
+    tmem_cp_powers(sfa, sdesc_powers(sw));
+    tmem_cp_powers(sfb, sdesc_powers(sx + MX_SCALE_BYTES));
+    if (XC == 8) tmem_cp_powers(sfb + 4, sdesc_powers(sx));
+    tmem_cp_powers(sfa + 4, sdesc_powers(sw + 512));
+    tmem_cp_powers(sfb + XC, sdesc_powers(sx + MX_SCALE_BYTES + 512));
+    if (XC == 8) tmem_cp_powers(sfb + XC + 4, sdesc_powers(sx + 512));
+    const uint64_t da = sdesc_k128(sw + MX_SCALE_BYTES), db = sdesc_k128(sx + 2 * MX_SCALE_BYTES);
+    if (ni == 4) {
+        mma_mxf4(tmem, da, db, id0, sfa, sfb, add);
+        mma_mxf4(tmem, da + 2, db + 2, id1, sfa, sfb, 1u);
+        mma_mxf4(tmem, da + 4, db + 4, id0, sfa + 4, sfb + XC, 1u);
+        mma_mxf4(tmem, da + 6, db + 6, id1, sfa + 4, sfb + XC, 1u);
+    } else {
+        mma_mxf4(tmem, da, db, id0, sfa, sfb, add);
+        if (ni > 1) mma_mxf4(tmem, da + 2, db + 2, id1, sfa, sfb, 1u);
+        if (ni > 2) mma_mxf4(tmem, da + 4, db + 4, id0, sfa + 4, sfb + XC, 1u);
+    }
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four floats at this CTA's shared address `at` in the cluster's CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster(uint32_t at, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 t;\n\tmapa.shared::cluster.u32 t, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [t];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(at), "r"(rank)
+        : "memory");
+    return v;
+}
 
 __device__ __forceinline__ float mx_act(float v, int act) {
     return act ? (v > 0.0f ? v * v : (v != v ? v : 0.0f)) : v;
 }
+template <typename O>
+struct MxOut;
+template <>
+struct MxOut<float> {
+    static __device__ __forceinline__ float one(float v) { return v; }
+};
+template <>
+struct MxOut<__half> {
+    static __device__ __forceinline__ __half one(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ uint32_t two(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *(const uint32_t *)&h;
+    }
+};
+template <>
+struct MxOut<__nv_bfloat16> {
+    static __device__ __forceinline__ __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ uint32_t two(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *(const uint32_t *)&h;
+    }
+};
+
+// Sixteen tokens (from column c of the tile, of `rows`) of a warp's 32 outputs, lane
+// n's in v.  16-bit types: neighbouring lanes trade halves, so that each stores two
+// outputs of every other token.
+template <typename O>
+__device__ __forceinline__ void store16(O *y, int64_t ldy, int c, int rows, int n, int N, bool pack, int act, float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = mx_act(v[j], act);
+    if constexpr (sizeof(O) == 2) {
+        if (pack) {
+            const int odd = threadIdx.x & 1;
+            O *z = y + n - odd + (int64_t)(c + odd) * ldy;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                const uint32_t w = odd ? MxOut<O>::two(got, v[j + 1]) : MxOut<O>::two(v[j], got);
+                if (c + j + odd < rows) {
+                    if ((n | 1) < N) *(uint32_t *)(z + (int64_t)j * ldy) = w;
+                    else if ((n & ~1) < N) z[(int64_t)j * ldy] = MxOut<O>::one(odd ? got : v[j]);
+                }
+            }
+            return;
+        }
+    }
+    if (n < N) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (c + j < rows) y[n + (int64_t)(c + j) * ldy] = MxOut<O>::one(v[j]);
+    }
+}
+// Four neighbouring outputs from n on of one token.
+template <typename O>
+__device__ __forceinline__ void store4(O *y, int n, int N, bool pack, int act, float4 s) {
+    const float v[4] = {mx_act(s.x, act), mx_act(s.y, act), mx_act(s.z, act), mx_act(s.w, act)};
+    if (pack && n + 3 < N) {
+        if constexpr (sizeof(O) == 2) *(uint2 *)(y + n) = make_uint2(MxOut<O>::two(v[0], v[1]), MxOut<O>::two(v[2], v[3]));
+        else *(float4 *)(y + n) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < N) y[n + j] = MxOut<O>::one(v[j]);
+    }
+}
+
+// A tile: its rows of w, its tokens, and how many rows of x's one or two records of
+// 128 hold them, padded to 16.
+struct MxTile {
+    int rt, b0, rows, npad, r0, r1;
+    __device__ __forceinline__ MxTile(const MxLinearArgs &a, int t) {
+        const int bt = t / a.rtiles;
+        rt = t - bt * a.rtiles;
+        b0 = bt * a.nt;
+        rows = min(a.nt, a.p.B - b0);
+        npad = (rows + 15) & ~15;
+        r0 = min(npad, MX_TILE_M);
+        r1 = npad - r0;
+    }
+};
 
 template <typename O>
 __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_constant__ MxLinearArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[MXL_MAX_STAGES], empty[MXL_MAX_STAGES], done;
-    __shared__ uint32_t tmem_slot, s_abort, s_ok;
+    __shared__ uint64_t full[MXL_MAX_STAGES], empty[MXL_MAX_STAGES], acc_full, acc_empty;
+    __shared__ uint32_t tmem_slot, s_abort, s_ok[2];
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = a.stages, kt = a.kt;
-    const int rt = blockIdx.x, b0 = blockIdx.y * a.nt;
-    const int rows = min(a.nt, a.p.B - b0);       // tokens of this tile
-    const int npad = (rows + 15) & ~15;
-    const uint32_t stage_bytes = MX_TILE_BYTES + a.xbytes;
+    const int S = a.stages, split = a.split;
+    const int first = blockIdx.x / split, rank = blockIdx.x - first * split, step = gridDim.x / split;
+    const int k0 = rank * a.kt / split, kn = (rank + 1) * a.kt / split - k0;  // this CTA's column tiles
     volatile uint32_t *abort_flag = &s_abort;
 
     if (threadIdx.x == 0) {
@@ -97,7 +219,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        mbar_init(&done, 1);
+        mbar_init(&acc_full, 1);
+        mbar_init(&acc_empty, MXL_EPI_WARPS);
         s_abort = 0u;
         fence_barrier_init();
     }
@@ -112,104 +235,160 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint8_t *w = a.p.w + (int64_t)rt * kt * MX_TILE_BYTES;
-            const uint8_t *x0 = a.p.x + (int64_t)(b0 / MX_TILE_M) * kt * MX_TILE_BYTES;
-            const uint8_t *x1 = x0 + (int64_t)kt * MX_TILE_BYTES;
-            const uint32_t n0 = (uint32_t)min(npad, MX_TILE_M) * 128u, n1 = (uint32_t)max(npad - MX_TILE_M, 0) * 128u;
-            const uint32_t bytes = MX_TILE_BYTES + MX_SCALE_BYTES + n0 + (n1 ? MX_SCALE_BYTES + n1 : 0u);
-            auto load_w = [&](int k, int st) {
-                mbar_expect_tx(&full[st], bytes);
-                bulk_g2s(base + st * stage_bytes, w + (int64_t)k * MX_TILE_BYTES, MX_TILE_BYTES, &full[st]);
+            auto load_w = [&](const MxTile &t, int k, int st) {
+                mbar_expect_tx(&full[st], MX_TILE_BYTES + MX_SCALE_BYTES * (t.r1 ? 2 : 1) + (uint32_t)t.npad * 128u);
+                bulk_g2s(base + st * a.stage_bytes, a.p.w + ((int64_t)t.rt * a.kt + k0 + k) * MX_TILE_BYTES, MX_TILE_BYTES,
+                         &full[st]);
             };
-            auto load_x = [&](int k, int st) {
-                uint8_t *to = base + st * stage_bytes + MX_TILE_BYTES;
-                const int64_t at = (int64_t)k * MX_TILE_BYTES;
-                bulk_g2s(to + MX_SCALE_BYTES, x0 + at, MX_SCALE_BYTES + n0, &full[st]);
+            auto load_x = [&](const MxTile &t, int k, int st) {
+                // powers of the second record, powers of the first, codes of both
+                uint8_t *to = base + st * a.stage_bytes + MX_TILE_BYTES;
+                const uint8_t *x0 = a.p.x + ((int64_t)(t.b0 / MX_TILE_M) * a.kt + k0 + k) * MX_TILE_BYTES;
+                const uint32_t n0 = (uint32_t)t.r0 * 128u, n1 = (uint32_t)t.r1 * 128u;
+                bulk_g2s(to + MX_SCALE_BYTES, x0, MX_SCALE_BYTES + n0, &full[st]);
                 if (n1) {
-                    bulk_g2s(to, x1 + at, MX_SCALE_BYTES, &full[st]);
-                    bulk_g2s(to + 2 * MX_SCALE_BYTES + n0, x1 + at + MX_SCALE_BYTES, n1, &full[st]);
+                    const uint8_t *x1 = x0 + (int64_t)a.kt * MX_TILE_BYTES;
+                    bulk_g2s(to, x1, MX_SCALE_BYTES, &full[st]);
+                    bulk_g2s(to + 2 * MX_SCALE_BYTES + n0, x1 + MX_SCALE_BYTES, n1, &full[st]);
                 }
             };
-            const int npre = min(S, kt);
-            for (int k = 0; k < npre; ++k) load_w(k, k);
-            pdl_wait();
-            for (int k = 0; k < npre; ++k) load_x(k, k);
-            int k = npre;
-            for (; k < kt; ++k) {
-                const int st = k % S;
-                if (!mbar_wait(&empty[st], (uint32_t)(k / S - 1) & 1u, abort_flag)) {
-                    *abort_flag = 1u;
-                    atomicOr(a.p.err, ERR_TIMEOUT);
-                    break;
+            const int npre = min(S, kn);  // of the first tile
+            {
+                const MxTile t(a, first);
+                for (int k = 0; k < npre; ++k) load_w(t, k, k);
+                pdl_wait();
+                for (int k = 0; k < npre; ++k) load_x(t, k, k);
+            }
+            int q = 0;
+            bool ok = true;
+            for (int i = first; i < a.tiles && ok; i += step) {
+                const MxTile t(a, i);
+                for (int k = 0; k < kn; ++k, ++q) {
+                    if (q < npre) continue;
+                    const int st = q % S;
+                    if (q >= S && !mbar_wait(&empty[st], (uint32_t)(q / S - 1) & 1u, abort_flag)) {
+                        *abort_flag = 1u;
+                        atomicOr(a.p.err, ERR_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
+                    load_w(t, k, st);
+                    load_x(t, k, st);
                 }
-                load_w(k, st);
-                load_x(k, st);
             }
             // no copy may be in flight when the CTA ends
-            for (int j = max(0, k - S); j < k; ++j)
+            for (int j = max(0, q - S); j < q; ++j)
                 if (!mbar_wait_any(&full[j % S], (uint32_t)(j / S) & 1u)) break;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id0 = idesc_mxf4(npad, 0), id1 = idesc_mxf4(npad, 1);
-            const uint32_t xsf = npad > MX_TILE_M ? 8u : 4u;  // columns of one chunk of x's powers
-            bool ok = true;
-            for (int k = 0; k < kt; ++k) {
-                const int st = k % S;
-                if (!mbar_wait(&full[st], (uint32_t)(k / S) & 1u, abort_flag)) {
+        bool ok = true;
+        int q = 0, n = 0;
+        // a last tile of K % 256 columns: the instructions past them would add zeros
+        const int last = min(4, (a.p.K - (k0 + kn - 1) * MX_TILE_K + 63) / 64);
+        for (int i = first; i < a.tiles && ok; i += step, ++n) {
+            const MxTile t(a, i);
+            const uint32_t id0 = idesc_mxf4(t.npad, 0), id1 = idesc_mxf4(t.npad, 1);
+            if (n > 0 && !mbar_wait(&acc_empty, (uint32_t)(n - 1) & 1u, abort_flag)) {
+                ok = false;
+                break;
+            }
+            for (int k = 0; k < kn; ++k, ++q) {
+                const int st = q % S;
+                if (!mbar_wait(&full[st], (uint32_t)(q / S) & 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sw = smem_u32(base + st * stage_bytes), sx = sw + MX_TILE_BYTES;
-                const uint32_t sfa = tmem + a.sfcol + (uint32_t)st * 24u, sfb = sfa + 8u;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    tmem_cp_powers(sfa + h * 4, sdesc_powers(sw + h * 512));
-                    tmem_cp_powers(sfb + h * xsf, sdesc_powers(sx + MX_SCALE_BYTES + h * 512));
-                    if (npad > MX_TILE_M) tmem_cp_powers(sfb + h * xsf + 4, sdesc_powers(sx + h * 512));
+                const uint32_t sw = smem_u32(base + st * a.stage_bytes), sx = sw + MX_TILE_BYTES;
+                const uint32_t sfa = tmem + (uint32_t)a.nt + (uint32_t)st * MXL_SF, sfb = sfa + 8u;
+                if (elect_one()) {
+                    const int ni = k + 1 < kn ? 4 : last;
+                    if (t.r1) issue_stage<8>(tmem, sw, sx, sfa, sfb, id0, id1, k > 0, ni);
+                    else issue_stage<4>(tmem, sw, sx, sfa, sfb, id0, id1, k > 0, ni);
+                    mma_commit(&empty[st]);
+                    if (k + 1 == kn) mma_commit(&acc_full);
                 }
-                // a last tile of K % 256 columns: the instructions past them would add zeros
-                const int ni = min(4, (a.p.K - k * MX_TILE_K + 63) / 64);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < ni)
-                        mma_mxf4(tmem, sdesc_k128(sw + MX_SCALE_BYTES + i * 32), sdesc_k128(sx + 2 * MX_SCALE_BYTES + i * 32),
-                                 (i & 1) ? id1 : id0, sfa + (i >> 1) * 4, sfb + (i >> 1) * xsf, (k | i) ? 1u : 0u);
-                mma_commit(&empty[st]);
+                __syncwarp();
             }
-            if (!ok) {
-                *abort_flag = 1u;
-                atomicOr(a.p.err, ERR_TIMEOUT);
-            }
-            mma_commit(&done);
-            if (!ok) mbar_wait_any(&done, 0u);  // no product may be in flight when the CTA ends
+        }
+        if (!ok && elect_one()) {
+            *abort_flag = 1u;
+            atomicOr(a.p.err, ERR_TIMEOUT);
+            // no product may be in flight when the CTA ends
+            mma_commit(&acc_full);
+            mbar_wait_any(&acc_full, (uint32_t)n & 1u);
         }
     } else {
         pdl_wait();  // y may have readers before the kernel this one follows
-        const int et = threadIdx.x - 64, qd = warp & 3, grp = (warp - 2) >> 2;
-        if (et == 0) s_ok = mbar_wait(&done, 0u, abort_flag) ? 1u : 0u;
-        named_bar(1, 32 * MXL_EPI_WARPS);
-        if (s_ok) {
-            (void)mbar_try_wait(&done, 0u);
-            tc_fence_after();
-            const int n = rt * MX_TILE_M + qd * 32 + lane;
-            O *y = (O *)a.p.y + (int64_t)b0 * a.p.ldy + n;
-            for (int c = grp * 16; c < npad; c += 16 * (MXL_EPI_WARPS / 4)) {
-                float v[16];
-                tmem_ld16(tmem + ((uint32_t)(qd * 32) << 16) + (uint32_t)c, v);
-                if (n < a.p.N) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < rows) y[(int64_t)(c + j) * a.p.ldy] = mx_out<O>(mx_act(v[j], a.p.act));
+        const int qd = warp & 3, grp = (warp - 2) >> 2, row = qd * 32 + lane;
+        float *part = (float *)base;  // split: [npad][128] partial sums, over the ring once it is done with
+        int n = 0;
+        for (int i = first; i < a.tiles; i += step, ++n) {
+            const MxTile t(a, i);
+            if (threadIdx.x == 64) {
+                s_ok[n & 1] = mbar_wait(&acc_full, (uint32_t)n & 1u, abort_flag) ? 1u : 0u;
+                if (!s_ok[n & 1]) {
+                    *abort_flag = 1u;
+                    atomicOr(a.p.err, ERR_TIMEOUT);
                 }
             }
-        } else if (et == 0) {
-            *abort_flag = 1u;
-            atomicOr(a.p.err, ERR_TIMEOUT);
+            named_bar(1, MXL_EPI_THREADS);
+            if (!s_ok[n & 1]) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(qd * 32) << 16);
+            float v[MXL_CHUNKS][16];
+#pragma unroll
+            for (int h = 0; h < MXL_CHUNKS; ++h) {
+                const int c = (h * (MXL_EPI_WARPS / 4) + grp) * 16;
+                if (c < t.npad) tmem_ld16(acc + (uint32_t)c, v[h]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty);
+            O *y = (O *)a.p.y + (int64_t)t.b0 * a.p.ldy;
+#pragma unroll
+            for (int h = 0; h < MXL_CHUNKS; ++h) {
+                const int c = (h * (MXL_EPI_WARPS / 4) + grp) * 16;
+                if (c >= t.npad) break;
+                if (split > 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(c + j) * MX_TILE_M + row] = v[h][j];
+                } else {
+                    store16<O>(y, a.p.ldy, c, t.rows, t.rt * MX_TILE_M + row, a.p.N, a.pack, a.p.act, v[h]);
+                }
+            }
         }
     }
     __syncwarp();
+    if (split > 1) {
+        // one tile a cluster: every CTA adds its share of the tokens, four outputs a thread
+        const MxTile t(a, first);
+        cluster_sync();
+        if (warp >= 2) {
+            const int n = t.rt * MX_TILE_M + lane * 4, c1 = (rank + 1) * t.rows / split;
+            O *y = (O *)a.p.y + (int64_t)t.b0 * a.p.ldy;
+            for (int c = rank * t.rows / split + warp - 2; c < c1; c += 2 * MXL_EPI_WARPS) {
+                const int d = c + MXL_EPI_WARPS;  // a second token, its loads beside the first's
+                const uint32_t at = smem_u32(base) + (uint32_t)(c * MX_TILE_M + lane * 4) * 4u;
+                float4 v[2][MXL_MAX_SPLIT];
+#pragma unroll
+                for (int s = 0; s < MXL_MAX_SPLIT; ++s)
+                    if (s < split) {
+                        v[0][s] = ld_cluster(at, (uint32_t)s);
+                        if (d < c1) v[1][s] = ld_cluster(at + MXL_EPI_WARPS * MX_TILE_M * 4u, (uint32_t)s);
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 sum = v[h][0];
+#pragma unroll
+                    for (int s = 1; s < MXL_MAX_SPLIT; ++s)
+                        if (s < split) sum.x += v[h][s].x, sum.y += v[h][s].y, sum.z += v[h][s].z, sum.w += v[h][s].w;
+                    if (h == 0 || d < c1) store4<O>(y + (int64_t)(h ? d : c) * a.p.ldy, n, a.p.N, a.pack, a.p.act, sum);
+                }
+            }
+        }
+        cluster_sync();  // no CTA leaves while its partial sums are read
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -218,35 +397,75 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
     }
 }
 
+namespace {
+
+// How many clusters of s CTAs, one CTA a SM, the current device runs at once.
+int max_clusters(const void *fn, int s, cudaError_t *e) {
+    static int known[64][MXL_MAX_SPLIT + 1];  // per device; 0: not asked yet (a repeated answer is the same)
+    int dev = 0;
+    cudaError_t r = cudaGetDevice(&dev);
+    if (r == cudaSuccess && dev < 64 && known[dev][s]) return known[dev][s];
+    int n = 0;
+    if (r == cudaSuccess) r = ensure_smem_attr(fn, (int)MXL_SMEM_MAX);
+    if (r == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)s * 256);
+        cfg.blockDim = dim3(MXL_THREADS);
+        cfg.dynamicSmemBytes = MXL_SMEM_MAX;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)s;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        r = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+    }
+    if (r != cudaSuccess) *e = r;
+    else if (dev < 64) known[dev][s] = n;
+    return n;
+}
+
+}  // namespace
+
 void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cudaError_t *e) {
-    MxLinearArgs a;
-    a.p = p;
-    a.kt = (p.K + MX_TILE_K - 1) / MX_TILE_K;
-    a.nt = std::min(256, (p.B + 15) & ~15);
-    a.xbytes = 2 * MX_SCALE_BYTES + (uint32_t)a.nt * 128u;
-    const uint32_t stage = MX_TILE_BYTES + a.xbytes;
-    a.stages = (int)std::min<uint32_t>(4, (MXL_SMEM_MAX - 1024) / stage);
-    a.sfcol = (uint32_t)a.nt;
-    a.ncols = 32;
-    while (a.ncols < a.sfcol + 24u * a.stages) a.ncols <<= 1;
-    // A CTA's part of the SM's shared memory is at least its part of tensor memory,
-    // so that CTAs that fit beside each other never wait for columns.
-    const uint32_t smem = std::min(MXL_SMEM_MAX, std::max(1024 + a.stages * stage, a.ncols * 456u));
     const void *fn = type == MX_F32   ? (const void *)mx_linear_kernel<float>
                      : type == MX_F16 ? (const void *)mx_linear_kernel<__half>
                                       : (const void *)mx_linear_kernel<__nv_bfloat16>;
-    cudaError_t r = ensure_smem_attr(fn, (int)smem);
+    MxLinearArgs a;
+    a.p = p;
+    a.kt = (p.K + MX_TILE_K - 1) / MX_TILE_K;
+    a.nt = std::min(MXL_TOKENS, (p.B + 15) & ~15);
+    a.rtiles = (p.N + MX_TILE_M - 1) / MX_TILE_M;
+    a.tiles = a.rtiles * ((p.B + a.nt - 1) / a.nt);
+    a.stage_bytes = MX_TILE_BYTES + 2 * MX_SCALE_BYTES + (uint32_t)a.nt * 128u;
+    a.stages = std::min({MXL_MAX_STAGES, (int)((MXL_SMEM_MAX - 1024) / a.stage_bytes), (512 - a.nt) / (int)MXL_SF});
+    a.ncols = 512;
+    const int size = type == MX_F32 ? 4 : 2;
+    // The widest cluster under which every tile has one and every CTA two column tiles.
+    a.split = 1;
+    int clusters = max_clusters(fn, 1, e);
+    for (int s = 2; s <= MXL_MAX_SPLIT && 2 * s <= a.kt && *e == cudaSuccess; ++s) {
+        const int n = max_clusters(fn, s, e);
+        if (a.tiles <= n) a.split = s, clusters = n;
+    }
+    if (*e != cudaSuccess) return;
+    const int neigh = a.split > 1 ? 4 * size : 4;
+    a.pack = (uintptr_t)p.y % neigh == 0 && p.ldy * size % neigh == 0;
+    cudaError_t r = ensure_smem_attr(fn, (int)MXL_SMEM_MAX);
     if (r == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((p.N + MX_TILE_M - 1) / MX_TILE_M), (unsigned)((p.B + a.nt - 1) / a.nt));
+        cfg.gridDim = dim3((unsigned)(std::min(a.tiles, clusters) * a.split));
         cfg.blockDim = dim3(MXL_THREADS);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = MXL_SMEM_MAX;
         cfg.stream = lc.stream;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)a.split;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
-        cfg.numAttrs = lc.pdl ? 1 : 0;
+        cfg.numAttrs = lc.pdl ? 2 : 1;
         void *args[] = {&a};
         r = cudaLaunchKernelExC(&cfg, fn, args);
     }
