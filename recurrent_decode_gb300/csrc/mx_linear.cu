@@ -187,6 +187,15 @@ __device__ __forceinline__ void store4(O *y, int n, int N, bool pack, int act, f
     }
 }
 
+// Position in the ring: stage and the parity of its current use.
+struct MxRing {
+    int st = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++st == stages) st = 0, parity ^= 1u;
+    }
+};
+
 // A tile: its rows of w, its tokens, and how many rows of x's one or two records of
 // 128 hold them, padded to 16.
 struct MxTile {
@@ -202,6 +211,29 @@ struct MxTile {
     }
 };
 
+// The products of one tile, by a whole warp: what the instructions take stays
+// uniform over it, and one elected lane issues them.  (Issued under a branch on the
+// lane index, with a division for the ring position, a stage took 1.5 times as long.)
+template <int XC>
+__device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32_t sf0, uint32_t stage_bytes, int S, int kn,
+                                           int last, int npad, MxRing &ring, uint64_t *full, uint64_t *empty,
+                                           uint64_t *acc_full, volatile uint32_t *abort_flag) {
+    const uint32_t id0 = idesc_mxf4(npad, 0), id1 = idesc_mxf4(npad, 1);
+    for (int k = 0; k < kn; ++k) {
+        if (!mbar_wait(&full[ring.st], ring.parity, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t sw = ring0 + (uint32_t)ring.st * stage_bytes, sfa = sf0 + (uint32_t)ring.st * MXL_SF;
+        if (elect_one()) {
+            issue_stage<XC>(tmem, sw, sw + MX_TILE_BYTES, sfa, sfa + 8u, id0, id1, k > 0, k + 1 < kn ? 4 : last);
+            mma_commit(&empty[ring.st]);
+            if (k + 1 == kn) mma_commit(acc_full);
+        }
+        __syncwarp();
+        ring.next(S);
+    }
+    return true;
+}
+
 template <typename O>
 __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_constant__ MxLinearArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -214,6 +246,11 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
     const int k0 = rank * a.kt / split, kn = (rank + 1) * a.kt / split - k0;  // this CTA's column tiles
     volatile uint32_t *abort_flag = &s_abort;
 
+    auto load_w = [&](const MxTile &t, int k, int st) {
+        mbar_expect_tx(&full[st], MX_TILE_BYTES + MX_SCALE_BYTES * (t.r1 ? 2 : 1) + (uint32_t)t.npad * 128u);
+        bulk_g2s(base + st * a.stage_bytes, a.p.w + ((int64_t)t.rt * a.kt + k0 + k) * MX_TILE_BYTES, MX_TILE_BYTES, &full[st]);
+    };
+    const int npre = min(S, kn);  // stages of the first tile whose weights are requested at once
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
@@ -223,6 +260,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
         mbar_init(&acc_empty, MXL_EPI_WARPS);
         s_abort = 0u;
         fence_barrier_init();
+        const MxTile t(a, first);
+        for (int k = 0; k < npre; ++k) load_w(t, k, k);
     }
     if (warp == 1) {
         tmem_alloc(&tmem_slot, a.ncols);
@@ -231,15 +270,10 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     if (warp == 0) {
         if (lane == 0) {
-            auto load_w = [&](const MxTile &t, int k, int st) {
-                mbar_expect_tx(&full[st], MX_TILE_BYTES + MX_SCALE_BYTES * (t.r1 ? 2 : 1) + (uint32_t)t.npad * 128u);
-                bulk_g2s(base + st * a.stage_bytes, a.p.w + ((int64_t)t.rt * a.kt + k0 + k) * MX_TILE_BYTES, MX_TILE_BYTES,
-                         &full[st]);
-            };
             auto load_x = [&](const MxTile &t, int k, int st) {
                 // powers of the second record, powers of the first, codes of both
                 uint8_t *to = base + st * a.stage_bytes + MX_TILE_BYTES;
@@ -252,28 +286,26 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
                     bulk_g2s(to + 2 * MX_SCALE_BYTES + n0, x1 + MX_SCALE_BYTES, n1, &full[st]);
                 }
             };
-            const int npre = min(S, kn);  // of the first tile
             {
                 const MxTile t(a, first);
-                for (int k = 0; k < npre; ++k) load_w(t, k, k);
                 pdl_wait();
                 for (int k = 0; k < npre; ++k) load_x(t, k, k);
             }
+            MxRing ring;
             int q = 0;
             bool ok = true;
             for (int i = first; i < a.tiles && ok; i += step) {
                 const MxTile t(a, i);
-                for (int k = 0; k < kn; ++k, ++q) {
+                for (int k = 0; k < kn; ++k, ++q, ring.next(S)) {
                     if (q < npre) continue;
-                    const int st = q % S;
-                    if (q >= S && !mbar_wait(&empty[st], (uint32_t)(q / S - 1) & 1u, abort_flag)) {
+                    if (q >= S && !mbar_wait(&empty[ring.st], ring.parity ^ 1u, abort_flag)) {
                         *abort_flag = 1u;
                         atomicOr(a.p.err, ERR_TIMEOUT);
                         ok = false;
                         break;
                     }
-                    load_w(t, k, st);
-                    load_x(t, k, st);
+                    load_w(t, k, ring.st);
+                    load_x(t, k, ring.st);
                 }
             }
             // no copy may be in flight when the CTA ends
@@ -282,34 +314,19 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
         }
     } else if (warp == 1) {
         bool ok = true;
-        int q = 0, n = 0;
+        int n = 0;
+        MxRing ring;
         // a last tile of K % 256 columns: the instructions past them would add zeros
         const int last = min(4, (a.p.K - (k0 + kn - 1) * MX_TILE_K + 63) / 64);
+        const uint32_t ring0 = smem_u32(base), sf0 = tmem + (uint32_t)a.nt;
         for (int i = first; i < a.tiles && ok; i += step, ++n) {
             const MxTile t(a, i);
-            const uint32_t id0 = idesc_mxf4(t.npad, 0), id1 = idesc_mxf4(t.npad, 1);
             if (n > 0 && !mbar_wait(&acc_empty, (uint32_t)(n - 1) & 1u, abort_flag)) {
                 ok = false;
                 break;
             }
-            for (int k = 0; k < kn; ++k, ++q) {
-                const int st = q % S;
-                if (!mbar_wait(&full[st], (uint32_t)(q / S) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t sw = smem_u32(base + st * a.stage_bytes), sx = sw + MX_TILE_BYTES;
-                const uint32_t sfa = tmem + (uint32_t)a.nt + (uint32_t)st * MXL_SF, sfb = sfa + 8u;
-                if (elect_one()) {
-                    const int ni = k + 1 < kn ? 4 : last;
-                    if (t.r1) issue_stage<8>(tmem, sw, sx, sfa, sfb, id0, id1, k > 0, ni);
-                    else issue_stage<4>(tmem, sw, sx, sfa, sfb, id0, id1, k > 0, ni);
-                    mma_commit(&empty[st]);
-                    if (k + 1 == kn) mma_commit(&acc_full);
-                }
-                __syncwarp();
-            }
+            ok = t.r1 ? issue_tile<8>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, ring, full, empty, &acc_full, abort_flag)
+                      : issue_tile<4>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, ring, full, empty, &acc_full, abort_flag);
         }
         if (!ok && elect_one()) {
             *abort_flag = 1u;
@@ -443,7 +460,8 @@ void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cu
     const int size = type == MX_F32 ? 4 : 2;
     // The widest cluster under which every tile has one and every CTA two column tiles.
     a.split = 1;
-    int clusters = max_clusters(fn, 1, e);
+    int clusters = std::max(1, max_clusters(fn, 1, e));
+    clusters = (a.tiles + (a.tiles + clusters - 1) / clusters - 1) / ((a.tiles + clusters - 1) / clusters);  // equal shares
     for (int s = 2; s <= MXL_MAX_SPLIT && 2 * s <= a.kt && *e == cudaSuccess; ++s) {
         const int n = max_clusters(fn, s, e);
         if (a.tiles <= n) a.split = s, clusters = n;
