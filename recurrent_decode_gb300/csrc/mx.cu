@@ -12,25 +12,68 @@
 
 namespace rk {
 
+// Eight neighbouring values of a row as a lane holds them between load and use: in
+// 16-bit types two a word, so that four lines in flight take 16 registers.
 template <int T>
 struct MxElem;
 template <>
 struct MxElem<MX_F32> {
     using type = float;
-    static __device__ __forceinline__ float up(float v) { return v; }
+    struct Eight {
+        float v[8];
+    };
+    static __device__ __forceinline__ void load(Eight &u, const float *p) { ld_v8(u.v, p); }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[8]) { st_v8(p, v); }
+    static __device__ __forceinline__ void set(Eight &u, int i, float v) { u.v[i] = v; }
+    static __device__ __forceinline__ uint32_t top(const Eight &u) { return mx_quad_top(u.v); }
+    static __device__ __forceinline__ float up(const Eight &u, int i) { return u.v[i]; }
     static __device__ __forceinline__ float down(float v) { return v; }
 };
-template <>
-struct MxElem<MX_F16> {
-    using type = __half;
-    static __device__ __forceinline__ float up(__half v) { return __half2float(v); }
-    static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+// 16-bit types.  Their bits without the sign order like their values (infinity and
+// NaN last), as pairs of unsigned halves.
+template <typename E>
+struct MxHalves {
+    using type = E;
+    struct Eight {
+        uint32_t w[4];
+    };
+    static __device__ __forceinline__ void load(Eight &u, const E *p) { *(uint4 *)u.w = *(const uint4 *)p; }
+    static __device__ __forceinline__ void set(Eight &u, int i, E v) { ((E *)u.w)[i] = v; }
+    static __device__ __forceinline__ uint32_t top_bits(const Eight &u) {
+        uint32_t m = __vmaxu2(__vmaxu2(u.w[0] & 0x7FFF7FFFu, u.w[1] & 0x7FFF7FFFu),
+                              __vmaxu2(u.w[2] & 0x7FFF7FFFu, u.w[3] & 0x7FFF7FFFu));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        return max(m >> 16, m & 0xFFFFu);
+    }
 };
 template <>
-struct MxElem<MX_BF16> {
-    using type = __nv_bfloat16;
-    static __device__ __forceinline__ float up(__nv_bfloat16 v) { return __bfloat162float(v); }
+struct MxElem<MX_F16> : MxHalves<__half> {
+    static __device__ __forceinline__ uint32_t top(const Eight &u) {
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top_bits(u))));
+    }
+    static __device__ __forceinline__ float up(const Eight &u, int i) { return __half2float(((const __half *)u.w)[i]); }
+    static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ void store(__half *p, const float (&v)[8]) {
+        __half2 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        *(uint4 *)p = *(const uint4 *)h;
+    }
+};
+template <>
+struct MxElem<MX_BF16> : MxHalves<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t top(const Eight &u) { return top_bits(u) << 16; }
+    static __device__ __forceinline__ float up(const Eight &u, int i) {
+        return __uint_as_float(i & 1 ? u.w[i >> 1] & 0xFFFF0000u : u.w[i >> 1] << 16);
+    }
     static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
+        __nv_bfloat162 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        *(uint4 *)p = *(const uint4 *)h;
+    }
 };
 
 struct MxRowsParams {
@@ -46,104 +89,118 @@ constexpr int MXQ_THREADS = 256;
 constexpr int MXQ_LINES = 4;  // lines of a warp at most, their loads issued together
 constexpr int MXQ_MANY = 152 * 8 * 8;  // from here on (eight warps on each SM eight times over) a warp takes them all
 
-// Where lane's eight values of a line lie in its tile.
-__device__ __forceinline__ int64_t mx_tile_at(int r, int t, int kt) {
-    return ((int64_t)(r / MX_TILE_M) * kt + t) * MX_TILE_BYTES;
-}
-__device__ __forceinline__ int mx_code_at(int rr, int lane) {
-    return (int)MX_SCALE_BYTES + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4;
-}
-__device__ __forceinline__ int mx_power_at(int rr, int blk) {
-    return (blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4 + (blk & 3);
-}
+// Where a line lies: its values, a lane's four bytes of codes, the word of a half
+// line's powers.  Walks on line by line.
+template <typename E>
+struct MxLine {
+    E *x;
+    uint8_t *code, *power;
+    int r, t;
+    __device__ __forceinline__ MxLine(const MxRowsParams &p, int line, int lane) {
+        r = line / p.kt;
+        t = line - r * p.kt;
+        row(p, lane);
+    }
+    __device__ __forceinline__ void row(const MxRowsParams &p, int lane) {
+        const int rr = r % MX_TILE_M, blk = lane >> 2;
+        uint8_t *tile = p.mx + ((int64_t)(r / MX_TILE_M) * p.kt + t) * MX_TILE_BYTES;
+        x = (E *)p.x + r * p.ld + (int64_t)t * MX_TILE_K;
+        code = tile + MX_SCALE_BYTES + rr * 128 + ((blk ^ (rr & 7)) << 4) + (lane & 3) * 4;
+        power = tile + (blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4;
+    }
+    __device__ __forceinline__ void next(const MxRowsParams &p, int lane) {
+        if (++t < p.kt) {
+            x += MX_TILE_K;
+            code += MX_TILE_BYTES;
+            power += MX_TILE_BYTES;
+        } else {
+            t = 0;
+            ++r;
+            row(p, lane);
+        }
+    }
+    // how many of the line's 256 columns the matrix has
+    __device__ __forceinline__ int cols(const MxRowsParams &p) const { return (int)min((int64_t)MX_TILE_K, p.cols - (int64_t)t * MX_TILE_K); }
+};
 
 // A warp takes p.per consecutive lines (a line: 256 columns of a row), eight values a
 // lane.  Rows off the 16-byte grid are read value by value, neighbours by
 // neighbouring lanes, and turned through shared memory.
 template <int T>
 __global__ void __launch_bounds__(MXQ_THREADS) mx4_quantize_kernel(const MxRowsParams p) {
-    using E = typename MxElem<T>::type;
-    __shared__ float turn[MXQ_THREADS / 32][MX_TILE_K];
+    using L = MxElem<T>;
+    using E = typename L::type;
+    __shared__ __align__(16) E turn[MXQ_THREADS / 32][MX_TILE_K];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first = (blockIdx.x * (MXQ_THREADS / 32) + warp) * p.per;
     pdl_launch();  // a product of these rows may start fetching its weights
     const int n = min(p.per, p.lines - first);
     if (n <= 0) return;
-    const int r0 = first / p.kt, t0 = first - r0 * p.kt;
-    float v[MXQ_LINES][8];
-    int r = r0, t = t0;
+    typename L::Eight u[MXQ_LINES];
+    MxLine<E> at(p, first, lane);
+    const MxLine<E> start = at;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
         if (l >= n) break;
-        const int64_t c0 = (int64_t)t * MX_TILE_K;
-        const E *src = (const E *)p.x + r * p.ld + c0;
-        if (p.vec && c0 + lane * 8 + 8 <= p.cols) {
-            if constexpr (T == MX_F32) {
-                ld_v8(v[l], src + lane * 8);
-            } else {
-                alignas(16) E u[8];
-                *(uint4 *)u = *(const uint4 *)(src + lane * 8);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[l][i] = MxElem<T>::up(u[i]);
-            }
-        } else if (p.vec) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[l][i] = c0 + lane * 8 + i < p.cols ? MxElem<T>::up(src[lane * 8 + i]) : 0.0f;
+        const int cols = at.cols(p);
+        if (p.vec && lane * 8 + 8 <= cols) {
+            L::load(u[l], at.x + lane * 8);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[l][i] = c0 + i * 32 + lane < p.cols ? MxElem<T>::up(src[i * 32 + lane]) : 0.0f;
+            for (int i = 0; i < 8; ++i) {
+                const int c = p.vec ? lane * 8 + i : i * 32 + lane;
+                L::set(u[l], i, c < cols ? at.x[c] : L::down(0.0f));
+            }
         }
-        if (++t == p.kt) t = 0, ++r;
+        at.next(p, lane);
     }
-    r = r0, t = t0;
+    at = start;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
         if (l >= n) break;
         if (!p.vec) {
-            float *tw = turn[warp];
+            E *tw = turn[warp];
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tw[i * 32 + lane] = v[l][i];
+            for (int i = 0; i < 8; ++i) tw[i * 32 + lane] = ((const E *)&u[l])[i];
             __syncwarp();
-            *(float4 *)&v[l][0] = *(const float4 *)&tw[lane * 8];
-            *(float4 *)&v[l][4] = *(const float4 *)&tw[lane * 8 + 4];
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(u[l]) / 16; ++i) ((uint4 *)&u[l])[i] = ((const uint4 *)(tw + lane * 8))[i];
         }
-        const uint32_t s = mx_scale<MXFP4>(mx_quad_top(v[l]));
+        const uint32_t s = mx_scale<MXFP4>(L::top(u[l]));
         const float f = mx_inverse(s);  // a block without a number: its codes do not matter
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[l][i] *= f;
+        for (int i = 0; i < 8; ++i) v[i] = L::up(u[l], i) * f;
         // the powers of four blocks to one word, held by lanes 0 and 16
         uint32_t w = s | __shfl_down_sync(0xffffffffu, s, 4) << 8;
         w |= __shfl_down_sync(0xffffffffu, w, 8) << 16;
-        uint8_t *tile = p.mx + mx_tile_at(r, t, p.kt);
-        const int rr = r % MX_TILE_M;
-        *(uint32_t *)(tile + mx_code_at(rr, lane)) = fp4_pack8(v[l]);
-        if ((lane & 15) == 0) *(uint32_t *)(tile + mx_power_at(rr, lane >> 2)) = w;
-        if (++t == p.kt) t = 0, ++r;
+        *(uint32_t *)at.code = fp4_pack8(v);
+        if ((lane & 15) == 0) *(uint32_t *)at.power = w;
+        at.next(p, lane);
     }
 }
 
 template <int T>
 __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRowsParams p) {
-    using E = typename MxElem<T>::type;
-    __shared__ float turn[MXQ_THREADS / 32][MX_TILE_K];
+    using L = MxElem<T>;
+    using E = typename L::type;
+    __shared__ __align__(16) float turn[MXQ_THREADS / 32][MX_TILE_K];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first = (blockIdx.x * (MXQ_THREADS / 32) + warp) * p.per;
     const int n = min(p.per, p.lines - first);
     if (n <= 0) return;
-    const int r0 = first / p.kt, t0 = first - r0 * p.kt;
     uint32_t code[MXQ_LINES], s[MXQ_LINES];
-    int r = r0, t = t0;
+    MxLine<E> at(p, first, lane);
+    const MxLine<E> start = at;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
         if (l >= n) break;
-        const uint8_t *tile = p.mx + mx_tile_at(r, t, p.kt);
-        code[l] = *(const uint32_t *)(tile + mx_code_at(r % MX_TILE_M, lane));
-        s[l] = tile[mx_power_at(r % MX_TILE_M, lane >> 2)];
-        if (++t == p.kt) t = 0, ++r;
+        code[l] = *(const uint32_t *)at.code;
+        s[l] = at.power[(lane >> 2) & 3];
+        at.next(p, lane);
     }
-    r = r0, t = t0;
+    at = start;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
         if (l >= n) break;
@@ -152,21 +209,13 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRow
         const float f = s[l] == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s[l]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= f;
-        const int64_t c0 = (int64_t)t * MX_TILE_K;
-        E *dst = (E *)p.x + r * p.ld + c0;
-        if (p.vec && c0 + lane * 8 + 8 <= p.cols) {
-            if constexpr (T == MX_F32) {
-                st_v8(dst + lane * 8, v);
-            } else {
-                alignas(16) E u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = MxElem<T>::down(v[i]);
-                *(uint4 *)(dst + lane * 8) = *(const uint4 *)u;
-            }
+        const int cols = at.cols(p);
+        if (p.vec && lane * 8 + 8 <= cols) {
+            L::store(at.x + lane * 8, v);
         } else if (p.vec) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c0 + lane * 8 + i < p.cols) dst[lane * 8 + i] = MxElem<T>::down(v[i]);
+                if (lane * 8 + i < cols) at.x[lane * 8 + i] = L::down(v[i]);
         } else {
             float *tw = turn[warp];
             __syncwarp();
@@ -175,9 +224,9 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRow
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c0 + i * 32 + lane < p.cols) dst[i * 32 + lane] = MxElem<T>::down(tw[i * 32 + lane]);
+                if (i * 32 + lane < cols) at.x[i * 32 + lane] = L::down(tw[i * 32 + lane]);
         }
-        if (++t == p.kt) t = 0, ++r;
+        at.next(p, lane);
     }
 }
 

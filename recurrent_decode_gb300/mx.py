@@ -8,6 +8,7 @@ stream, and do not synchronise.
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 import torch
 
@@ -23,6 +24,8 @@ _MAX_DIM = 1 << 24  # RWKV7_MX_MAX_DIM
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
+_ROOM = 2 << 20  # 128 rows of 30,000 columns
+_kept = threading.local()  # (device, stream) -> bytes of _room
 _err: dict[int, torch.Tensor] = {}  # per device: the word in which kernels latch errors
 
 
@@ -35,8 +38,10 @@ def _err_word(dev: int) -> torch.Tensor:
     return w
 
 
-def _call(fn, dev: int, *args):
-    """fn(*args, stream, &message) on the current stream of device `dev`, with it current."""
+def _call(name: str, dev: int, *args):
+    """The library's `name`(*args, stream, &message) on the current stream of device
+    `dev`, with it current."""
+    fn = getattr(load_library(), name)
     msg = C.c_char_p()
     if dev == _current_device():
         rc = fn(*args, _raw_stream(dev), C.byref(msg))
@@ -45,6 +50,21 @@ def _call(fn, dev: int, *args):
             rc = fn(*args, _raw_stream(dev), C.byref(msg))
     if rc:
         raise RWKV7Error(rc, (msg.value or b"").decode())
+
+
+def _room(n: int, dev: int) -> torch.Tensor:
+    """n bytes for x quantised on the way.  Up to _ROOM of them are kept for the next
+    call of the same host thread on the same stream, whose kernels run after this
+    call's (an allocation between two launches costs 3 us, a small product takes 6);
+    a graph gets bytes of its own."""
+    if n > _ROOM or torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
+    key = dev, _raw_stream(dev)
+    rooms = _kept.__dict__
+    w = rooms.get(key)
+    if w is None:
+        w = rooms[key] = torch.empty(_ROOM, dtype=torch.uint8, device=f"cuda:{dev}")
+    return w
 
 
 def _rows(x, what: str):
@@ -92,13 +112,15 @@ class MX4Matrix:
     def dequantize(self, dtype=torch.float32, out=None):
         """The values it stands for (rwkv7_mx4_dequantize)."""
         if out is None:
-            if dtype not in _DTYPES:
+            rows, cols, ld, code = self.rows, self.cols, self.cols, _DTYPES.get(dtype)
+            if code is None:
                 raise TypeError("dtype must be float32, float16 or bfloat16")
-            out = torch.empty(self.rows, self.cols, dtype=dtype, device=self.data.device)
-        rows, cols, ld, code = _rows(out, "out")
-        if (rows, cols) != (self.rows, self.cols) or out.get_device() != self.data.get_device():
-            raise ValueError("out must have the matrix's shape and device")
-        _call(load_library().rwkv7_mx4_dequantize, out.get_device(), self.data.data_ptr(), rows, cols, out.data_ptr(),
+            out = torch.empty((rows, cols), dtype=dtype, device=self.data.device)
+        else:
+            rows, cols, ld, code = _rows(out, "out")
+            if rows != self.rows or cols != self.cols or out.get_device() != self.data.get_device():
+                raise ValueError("out must have the matrix's shape and device")
+        _call("rwkv7_mx4_dequantize", out.get_device(), self.data.data_ptr(), rows, cols, out.data_ptr(),
               code, ld)
         return out
 
@@ -116,7 +138,7 @@ def mx4_quantize(x, out: MX4Matrix | None = None) -> MX4Matrix:
         out = mx4_empty(rows, cols, x.device)
     elif out.shape != (rows, cols) or out.data.device != x.device:
         raise ValueError("out must have x's shape and device")
-    _call(load_library().rwkv7_mx4_quantize, x.get_device(), x.data_ptr(), code, rows, cols, ld, out.data.data_ptr())
+    _call("rwkv7_mx4_quantize", x.get_device(), x.data_ptr(), code, rows, cols, ld, out.data.data_ptr())
     return out
 
 
@@ -128,7 +150,8 @@ def mx4_linear(x, w: MX4Matrix, out=None, out_dtype=None, activation=None):
     rwkv7_mx4_linear."""
     if not isinstance(w, MX4Matrix):
         raise TypeError("w must be an MX4Matrix")
-    if activation not in _ACTIVATIONS:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
     dev = w.data.get_device()
     if isinstance(x, MX4Matrix):
@@ -141,20 +164,22 @@ def mx4_linear(x, w: MX4Matrix, out=None, out_dtype=None, activation=None):
         raise ValueError(f"x has {K} columns, w {w.cols}")
     if x_dev != dev:
         raise ValueError(f"x is on cuda:{x_dev}, w on cuda:{dev}")
-    if src is not None:
-        xq = mx4_empty(B, K, x.device)
+    device = w.data.device
+    data = xq.data if src is None else _room(_bytes(B, K), dev)
+    N = ldy = w.rows
     if out is None:
-        out_dtype = out_dtype or default
-        if out_dtype not in _DTYPES:
+        out_code = _DTYPES.get(out_dtype or default)
+        if out_code is None:
             raise TypeError("out_dtype must be float32, float16 or bfloat16")
-        out = torch.empty(B, w.rows, dtype=out_dtype, device=w.data.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    rows, cols, ldy, out_code = _rows(out, "out")
-    if rows != B or cols != w.rows or out.get_device() != dev:
-        raise ValueError(f"out must be [{B}, {w.rows}] on cuda:{dev}")
-    _call(load_library().rwkv7_mx4_linear, dev, src, code, ldx, xq.data.data_ptr(), B, w.data.data_ptr(), cols, K,
-          out.data_ptr(), out_code, ldy, _ACTIVATIONS[activation], _err_word(dev).data_ptr())
+        out = torch.empty((B, N), dtype=out_dtype or default, device=device)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        rows, cols, ldy, out_code = _rows(out, "out")
+        if rows != B or cols != N or out.get_device() != dev:
+            raise ValueError(f"out must be [{B}, {N}] on cuda:{dev}")
+    _call("rwkv7_mx4_linear", dev, src, code, ldx, data.data_ptr(), B, w.data.data_ptr(), N, K, out.data_ptr(), out_code,
+          ldy, act, _err_word(dev).data_ptr())
     return out
 
 
@@ -200,7 +225,7 @@ class StateCache:
             raise TypeError("a state cache lies on a CUDA device")
         self.err = torch.zeros(1, dtype=torch.int32, device=self.data.device)
 
-    def _states(self, fn, states, slots, entries):
+    def _states(self, name, states, slots, entries):
         wkv, att, ffn = states
         dev, L, H = self.data.device, self.n_layer, self.n_head
         for what, t in (("wkv", wkv), ("shift_att", att), ("shift_ffn", ffn)):
@@ -212,17 +237,17 @@ class StateCache:
         if wkv.shape != (L, n_slots, H, 64, 64) or att.shape != (L, n_slots, 64 * H) or ffn.shape != att.shape:
             raise ValueError(f"states must be wkv [{L}, slots, {H}, 64, 64] and two token shifts [{L}, slots, {64 * H}]")
         n = _pair_count(slots, entries, dev)
-        _call(fn, dev.index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
+        _call(name, dev.index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
               entries.data_ptr(), n, self.data.data_ptr(), self.n_entries, self.format, self.err.data_ptr())
 
     def save(self, states, slots, entries):
         """Keep the states of `slots` in `entries` (rwkv7_states_save).  states:
         (wkv [L, n_slots, H, 64, 64], shift_att, shift_ffn [L, n_slots, 64 H])."""
-        self._states(load_library().rwkv7_states_save, states, slots, entries)
+        self._states("rwkv7_states_save", states, slots, entries)
 
     def load(self, states, entries, slots):
         """Put the kept states of `entries` into `slots` (rwkv7_states_load)."""
-        self._states(load_library().rwkv7_states_load, states, slots, entries)
+        self._states("rwkv7_states_load", states, slots, entries)
 
     def check(self):
         """Wait for the stream and raise if a save or load had a bad or repeated index."""
