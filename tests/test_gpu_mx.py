@@ -446,3 +446,42 @@ def test_slots_of_a_context(fmt):
     with pytest.raises(rd.RWKV7Error):
         rd.Rwkv7._check(ctx, ctx.lib.rwkv7_slots_save(ctx.h, None, None, 1, cache.data.data_ptr(), 3, 1))
     ctx.close()
+
+
+@pytest.mark.parametrize("fmt", ["mxint8", "mxfp4"])
+def test_packed_prefix_cache(fmt):
+    """The prefix cache over packed entries: the longest stored prefix comes back as its
+    quantised state, the least recently used entry goes first."""
+    from recurrent_decode_gb300.prefix_cache import PackedPrefixStateCache
+    ctx, _, dims = gpu_ctx("tiny", 3)
+    cache = PackedPrefixStateCache(ctx, 2, fmt, block=8)
+    dev = lambda a: torch.from_numpy(a.copy()).cuda()  # noqa: E731
+    body = synth.prompt_tokens(dims.vocab, 1, 12)[0]
+    assert cache.restore(body, 1) == 0
+    assert cache.prefill(0, body, 0, dev) == 12  # stored at 8 and at 12
+    at12 = ctx.get_state(0)
+    assert len(cache) == 2 and cache.restore(body, 1) == 12
+    got = ctx.get_state(1)
+    assert np.array_equal(got[0].astype(np.float64), nearest(at12[0], fmt))
+    assert np.array_equal(got[1], at12[1]) and np.array_equal(got[2], at12[2])
+    other = np.concatenate([body[:9], body[:1]])
+    assert cache.restore(other, 2) == 8
+    cache.store(other, 2)  # evicts the entry after 12 tokens
+    assert cache.evictions == 1 and cache.restore(body, 1) == 8
+    ctx.synchronize()
+    ctx.close()
+
+
+def test_example_runs():
+    """The example on the tiny shape.  Rounding to MXFP4 is off by at most a fifth of a
+    value past the block's smallest steps and by a third of the block's largest in all;
+    independent errors of that size in both operands stay below 0.35 of a random sum, and
+    two products in a row below 0.6.  The states are 1/126 and a third of a block's
+    largest off, and the logits take them through one token."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import microscaled
+    r = microscaled.main(["--shape", "tiny", "--slots", "3", "--prefix", "40"])
+    assert 0 < r["mxint8"] < 0.01 and r["mxint8"] < r["mxfp4"] < 0.35
+    assert 0 < r["head"] < 0.35 and 0 < r["channel mix"] < 0.6
