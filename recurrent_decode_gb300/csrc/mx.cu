@@ -486,6 +486,7 @@ int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx
     if (activation != RWKV7_ACT_NONE && activation != RWKV7_ACT_RELU2)
         return mx_fail(err_msg, RWKV7_EINVAL, "unknown activation %lld", activation);
     if (B > 1 && ldy < N) return mx_fail(err_msg, RWKV7_EINVAL, "output row stride %lld is below N=%lld", ldy, N);
+    if (B > ((int64_t)1 << 42) / N) return mx_fail(err_msg, RWKV7_EINVAL, "an output of %lld x %lld is too large", B, N);
     if (B == 0) return RWKV7_OK;
     if (!d_x_mx || !d_w_mx || !d_y || !d_err) return mx_fail(err_msg, RWKV7_EINVAL, "null pointer argument");
     if ((uintptr_t)d_y % (y_dtype == RWKV7_F32 ? 4 : 2))

@@ -24,6 +24,8 @@
 // Each stage has columns of its own for its powers: they are overwritten only
 // after the commit that also frees the stage's shared memory.
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "mx.cuh"
 
@@ -81,16 +83,18 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 // One stage: its powers into tensor memory, then `ni` products of 64 columns each.
-// XC: tensor memory columns of x's powers for 128 columns of K (4 a record of 128 tokens).
+// XC: tensor memory columns of x's powers for 128 columns of K (4 a record of 128
+// tokens); off: the one of them in which the tile's first token lies.
 template <int XC>
 __device__ __forceinline__ void issue_stage(uint32_t tmem, uint32_t sw, uint32_t sx, uint32_t sfa, uint32_t sfb,
-                                            uint32_t id0, uint32_t id1, bool add, int ni) {
+                                            uint32_t off, uint32_t id0, uint32_t id1, bool add, int ni) {
     tmem_cp_powers(sfa, sdesc_powers(sw));
     tmem_cp_powers(sfb, sdesc_powers(sx + MX_SCALE_BYTES));
     if (XC == 8) tmem_cp_powers(sfb + 4, sdesc_powers(sx));
     tmem_cp_powers(sfa + 4, sdesc_powers(sw + 512));
     tmem_cp_powers(sfb + XC, sdesc_powers(sx + MX_SCALE_BYTES + 512));
     if (XC == 8) tmem_cp_powers(sfb + XC + 4, sdesc_powers(sx + 512));
+    sfb += off;
     const uint64_t da = sdesc_k128(sw + MX_SCALE_BYTES), db = sdesc_k128(sx + 2 * MX_SCALE_BYTES);
     if (ni == 4) {
         mma_mxf4(tmem, da, db, id0, sfa, sfb, add);
@@ -197,15 +201,17 @@ struct MxRing {
 };
 
 // A tile: its rows of w, its tokens, and how many rows of x's one or two records of
-// 128 hold them, padded to 16.
+// 128 hold them, padded to 16.  Tiles of 64 tokens start in the middle of every other
+// record (off = 64), larger ones where a record does.
 struct MxTile {
-    int rt, b0, rows, npad, r0, r1;
+    int rt, b0, rows, npad, off, r0, r1;
     __device__ __forceinline__ MxTile(const MxLinearArgs &a, int t) {
         const int bt = t / a.rtiles;
         rt = t - bt * a.rtiles;
         b0 = bt * a.nt;
         rows = min(a.nt, a.p.B - b0);
         npad = (rows + 15) & ~15;
+        off = b0 & (MX_TILE_M - 1);
         r0 = min(npad, MX_TILE_M);
         r1 = npad - r0;
     }
@@ -216,7 +222,7 @@ struct MxTile {
 // lane index, with a division for the ring position, a stage took 1.5 times as long.)
 template <int XC>
 __device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32_t sf0, uint32_t stage_bytes, int S, int kn,
-                                           int last, int npad, MxRing &ring, uint64_t *full, uint64_t *empty,
+                                           int last, int npad, uint32_t off, MxRing &ring, uint64_t *full, uint64_t *empty,
                                            uint64_t *acc_full, volatile uint32_t *abort_flag) {
     const uint32_t id0 = idesc_mxf4(npad, 0), id1 = idesc_mxf4(npad, 1);
     for (int k = 0; k < kn; ++k) {
@@ -224,7 +230,7 @@ __device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32
         tc_fence_after();
         const uint32_t sw = ring0 + (uint32_t)ring.st * stage_bytes, sfa = sf0 + (uint32_t)ring.st * MXL_SF;
         if (elect_one()) {
-            issue_stage<XC>(tmem, sw, sw + MX_TILE_BYTES, sfa, sfa + 8u, id0, id1, k > 0, k + 1 < kn ? 4 : last);
+            issue_stage<XC>(tmem, sw, sw + MX_TILE_BYTES, sfa, sfa + 8u, off, id0, id1, k > 0, k + 1 < kn ? 4 : last);
             mma_commit(&empty[ring.st]);
             if (k + 1 == kn) mma_commit(acc_full);
         }
@@ -279,7 +285,12 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
                 uint8_t *to = base + st * a.stage_bytes + MX_TILE_BYTES;
                 const uint8_t *x0 = a.p.x + ((int64_t)(t.b0 / MX_TILE_M) * a.kt + k0 + k) * MX_TILE_BYTES;
                 const uint32_t n0 = (uint32_t)t.r0 * 128u, n1 = (uint32_t)t.r1 * 128u;
-                bulk_g2s(to + MX_SCALE_BYTES, x0, MX_SCALE_BYTES + n0, &full[st]);
+                if (t.off == 0) {
+                    bulk_g2s(to + MX_SCALE_BYTES, x0, MX_SCALE_BYTES + n0, &full[st]);
+                } else {
+                    bulk_g2s(to + MX_SCALE_BYTES, x0, MX_SCALE_BYTES, &full[st]);
+                    bulk_g2s(to + 2 * MX_SCALE_BYTES, x0 + MX_SCALE_BYTES + t.off * 128, n0, &full[st]);
+                }
                 if (n1) {
                     const uint8_t *x1 = x0 + (int64_t)a.kt * MX_TILE_BYTES;
                     bulk_g2s(to, x1, MX_SCALE_BYTES, &full[st]);
@@ -325,8 +336,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
                 ok = false;
                 break;
             }
-            ok = t.r1 ? issue_tile<8>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, ring, full, empty, &acc_full, abort_flag)
-                      : issue_tile<4>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, ring, full, empty, &acc_full, abort_flag);
+            ok = t.r1 ? issue_tile<8>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag)
+                      : issue_tile<4>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag);
         }
         if (!ok && elect_one()) {
             *abort_flag = 1u;
@@ -416,15 +427,25 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
 
 namespace {
 
-// How many clusters of s CTAs, one CTA a SM, the current device runs at once.
-int max_clusters(const void *fn, int s, cudaError_t *e) {
-    static int known[64][MXL_MAX_SPLIT + 1];  // per device; 0: not asked yet (a repeated answer is the same)
+// How many clusters of 1 .. 8 CTAs, one CTA a SM, the current device runs at once.
+struct MxClusters {
+    int n[MXL_MAX_SPLIT + 1];
+};
+const MxClusters *max_clusters(const void *fn, cudaError_t *e) {
+    static MxClusters known[64];
+    static std::atomic<bool> done[64];
+    static std::mutex mu;
     int dev = 0;
-    cudaError_t r = cudaGetDevice(&dev);
-    if (r == cudaSuccess && dev < 64 && known[dev][s]) return known[dev][s];
-    int n = 0;
-    if (r == cudaSuccess) r = ensure_smem_attr(fn, (int)MXL_SMEM_MAX);
-    if (r == cudaSuccess) {
+    *e = cudaGetDevice(&dev);
+    if (*e != cudaSuccess) return nullptr;
+    if (dev >= 64) {
+        *e = cudaErrorInvalidDevice;
+        return nullptr;
+    }
+    if (done[dev].load(std::memory_order_acquire)) return &known[dev];
+    std::lock_guard<std::mutex> lk(mu);
+    *e = ensure_smem_attr(fn, (int)MXL_SMEM_MAX);
+    for (int s = 1; s <= MXL_MAX_SPLIT && *e == cudaSuccess; ++s) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)s * 256);
         cfg.blockDim = dim3(MXL_THREADS);
@@ -435,11 +456,40 @@ int max_clusters(const void *fn, int s, cudaError_t *e) {
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        r = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+        *e = cudaOccupancyMaxActiveClusters(&known[dev].n[s], fn, &cfg);
     }
-    if (r != cudaSuccess) *e = r;
-    else if (dev < 64) known[dev][s] = n;
-    return n;
+    if (*e != cudaSuccess) return nullptr;
+    if (known[dev].n[1] < 1) {
+        *e = cudaErrorInvalidConfiguration;
+        return nullptr;
+    }
+    done[dev].store(true, std::memory_order_release);
+    return &known[dev];
+}
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Tokens of a tile and CTAs of a cluster: the pair with the least estimate of a CTA's
+// time from its first stage on, in ns.  A stage takes 250 + 0.6 nt (copies, powers and
+// products; measured 260-290 at 16 and 64 tokens, 300 at 128, 390 at 256), a tile's end
+// 5 nt alone and 1000 + 17 nt in a cluster (partial sums through shared memory).
+// Measured, chosen / next best, us: 256 x 4096 (K 4096) 64 tokens alone 9.2 / 256 tokens
+// over 4 CTAs 11.1; 256 x 1024 (K 4096) 64 over 4 7.4 / 128 over 4 8.7; 512 x 4096 128
+// alone 10.3 / 256 over 2 11.2; 1024 x 2560 256 10.3 / 128 12.0; 37 x 1337 (K 1000) alone
+// 5.0 / over 2 5.8; 1 x 2560 (K 2560) over 5 5.5 / alone 7.2.
+void choose(MxLinearArgs &a, const MxClusters &most) {
+    const int whole = std::min(MXL_TOKENS, (a.p.B + 15) & ~15);
+    double best = 1e30;
+    for (int nt : {64, 128, whole}) {
+        if (nt > whole) continue;
+        const int tiles = a.rtiles * ceil_div(a.p.B, nt), rounds = ceil_div(tiles, most.n[1]);
+        for (int s = 1; s <= MXL_MAX_SPLIT && 2 * s <= std::max(2, a.kt); ++s) {
+            if (s > 1 && tiles > most.n[s]) continue;
+            const double t = s > 1 ? ceil_div(a.kt, s) * (250 + 0.6 * nt) + 1000 + 17.0 * nt
+                                   : rounds * (a.kt * (250 + 0.6 * nt) + 5.0 * nt);
+            if (t < best) best = t, a.nt = nt, a.split = s;
+        }
+    }
 }
 
 }  // namespace
@@ -450,29 +500,24 @@ void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cu
                                       : (const void *)mx_linear_kernel<__nv_bfloat16>;
     MxLinearArgs a;
     a.p = p;
-    a.kt = (p.K + MX_TILE_K - 1) / MX_TILE_K;
-    a.nt = std::min(MXL_TOKENS, (p.B + 15) & ~15);
-    a.rtiles = (p.N + MX_TILE_M - 1) / MX_TILE_M;
-    a.tiles = a.rtiles * ((p.B + a.nt - 1) / a.nt);
+    a.kt = ceil_div(p.K, MX_TILE_K);
+    a.rtiles = ceil_div(p.N, MX_TILE_M);
+    const MxClusters *most = max_clusters(fn, e);
+    if (!most) return;
+    choose(a, *most);
+    a.tiles = a.rtiles * ceil_div(p.B, a.nt);
+    // Every CTA as many tiles as the one with most.
+    const int clusters = a.split > 1 ? a.tiles : ceil_div(a.tiles, ceil_div(a.tiles, most->n[1]));
     a.stage_bytes = MX_TILE_BYTES + 2 * MX_SCALE_BYTES + (uint32_t)a.nt * 128u;
     a.stages = std::min({MXL_MAX_STAGES, (int)((MXL_SMEM_MAX - 1024) / a.stage_bytes), (512 - a.nt) / (int)MXL_SF});
     a.ncols = 512;
     const int size = type == MX_F32 ? 4 : 2;
-    // The widest cluster under which every tile has one and every CTA two column tiles.
-    a.split = 1;
-    int clusters = std::max(1, max_clusters(fn, 1, e));
-    clusters = (a.tiles + (a.tiles + clusters - 1) / clusters - 1) / ((a.tiles + clusters - 1) / clusters);  // equal shares
-    for (int s = 2; s <= MXL_MAX_SPLIT && 2 * s <= a.kt && *e == cudaSuccess; ++s) {
-        const int n = max_clusters(fn, s, e);
-        if (a.tiles <= n) a.split = s, clusters = n;
-    }
-    if (*e != cudaSuccess) return;
     const int neigh = a.split > 1 ? 4 * size : 4;
     a.pack = (uintptr_t)p.y % neigh == 0 && p.ldy * size % neigh == 0;
     cudaError_t r = ensure_smem_attr(fn, (int)MXL_SMEM_MAX);
     if (r == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(std::min(a.tiles, clusters) * a.split));
+        cfg.gridDim = dim3((unsigned)(clusters * a.split));
         cfg.blockDim = dim3(MXL_THREADS);
         cfg.dynamicSmemBytes = MXL_SMEM_MAX;
         cfg.stream = lc.stream;

@@ -178,6 +178,14 @@ def test_product_shapes_of_a_model(B, N, K):
     check_product(B, N, K, "fp16", "bf16", "relu2")
 
 
+@pytest.mark.parametrize("B,N,K", [(65, 100, 300), (80, 300, 2100), (191, 129, 600), (200, 4096, 260), (320, 200, 2048),
+                                   (500, 128, 5000), (1000, 130, 520), (700, 20000, 64), (257, 19456, 256)])
+def test_product_tiles_of_every_width(B, N, K):
+    """Few and many tiles, tokens that end inside one, alone and over a cluster."""
+    check_product(B, N, K, "bf16", "fp32", None)
+    check_product(B, N, K, "fp32", "fp16", "relu2", strided=True)
+
+
 @pytest.mark.parametrize("B", [3, 130])
 def test_product_of_whole_numbers_is_exact(B):
     """Values on the grid with equal powers: every sum is a whole number of quarters

@@ -64,6 +64,7 @@ def test_linear_refused(lib):
     f = lib.rwkv7_mx4_linear
     for bad in (dict(B=-1), dict(N=0), dict(K=0), dict(N=1 << 25), dict(B=1 << 25)):
         assert "at most" in refused(f, *call(**bad))
+    assert "too large" in refused(f, *call(B=1 << 24, N=1 << 24, ldy=1 << 24))
     assert "output dtype" in refused(f, *call(yt=7))
     assert "activation" in refused(f, *call(act=2))
     assert "output row stride" in refused(f, *call(ldy=7))
