@@ -12,70 +12,6 @@
 
 namespace rk {
 
-// Eight neighbouring values of a row as a lane holds them between load and use: in
-// 16-bit types two a word, so that four lines in flight take 16 registers.
-template <int T>
-struct MxElem;
-template <>
-struct MxElem<MX_F32> {
-    using type = float;
-    struct Eight {
-        float v[8];
-    };
-    static __device__ __forceinline__ void load(Eight &u, const float *p) { ld_v8(u.v, p); }
-    static __device__ __forceinline__ void store(float *p, const float (&v)[8]) { st_v8(p, v); }
-    static __device__ __forceinline__ void set(Eight &u, int i, float v) { u.v[i] = v; }
-    static __device__ __forceinline__ uint32_t top(const Eight &u) { return mx_quad_top(u.v); }
-    static __device__ __forceinline__ float up(const Eight &u, int i) { return u.v[i]; }
-    static __device__ __forceinline__ float down(float v) { return v; }
-};
-// 16-bit types.  Their bits without the sign order like their values (infinity and
-// NaN last), as pairs of unsigned halves.
-template <typename E>
-struct MxHalves {
-    using type = E;
-    struct Eight {
-        uint32_t w[4];
-    };
-    static __device__ __forceinline__ void load(Eight &u, const E *p) { *(uint4 *)u.w = *(const uint4 *)p; }
-    static __device__ __forceinline__ void set(Eight &u, int i, E v) { ((E *)u.w)[i] = v; }
-    static __device__ __forceinline__ uint32_t top_bits(const Eight &u) {
-        uint32_t m = __vmaxu2(__vmaxu2(u.w[0] & 0x7FFF7FFFu, u.w[1] & 0x7FFF7FFFu),
-                              __vmaxu2(u.w[2] & 0x7FFF7FFFu, u.w[3] & 0x7FFF7FFFu));
-        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        return max(m >> 16, m & 0xFFFFu);
-    }
-};
-template <>
-struct MxElem<MX_F16> : MxHalves<__half> {
-    static __device__ __forceinline__ uint32_t top(const Eight &u) {
-        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top_bits(u))));
-    }
-    static __device__ __forceinline__ float up(const Eight &u, int i) { return __half2float(((const __half *)u.w)[i]); }
-    static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
-    static __device__ __forceinline__ void store(__half *p, const float (&v)[8]) {
-        __half2 h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-        *(uint4 *)p = *(const uint4 *)h;
-    }
-};
-template <>
-struct MxElem<MX_BF16> : MxHalves<__nv_bfloat16> {
-    static __device__ __forceinline__ uint32_t top(const Eight &u) { return top_bits(u) << 16; }
-    static __device__ __forceinline__ float up(const Eight &u, int i) {
-        return __uint_as_float(i & 1 ? u.w[i >> 1] & 0xFFFF0000u : u.w[i >> 1] << 16);
-    }
-    static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
-        __nv_bfloat162 h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        *(uint4 *)p = *(const uint4 *)h;
-    }
-};
-
 struct MxRowsParams {
     void *x;  // [rows] at ld
     int64_t cols, ld;
@@ -167,15 +103,8 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_quantize_kernel(const MxRowsP
 #pragma unroll
             for (int i = 0; i < (int)sizeof(u[l]) / 16; ++i) ((uint4 *)&u[l])[i] = ((const uint4 *)(tw + lane * 8))[i];
         }
-        const uint32_t s = mx_scale<MXFP4>(L::top(u[l]));
-        const float f = mx_inverse(s);  // a block without a number: its codes do not matter
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = L::up(u[l], i) * f;
-        // the powers of four blocks to one word, held by lanes 0 and 16
-        uint32_t w = s | __shfl_down_sync(0xffffffffu, s, 4) << 8;
-        w |= __shfl_down_sync(0xffffffffu, w, 8) << 16;
-        *(uint32_t *)at.code = fp4_pack8(v);
+        uint32_t w;
+        *(uint32_t *)at.code = mx4_line<T>(u[l], w);
         if ((lane & 15) == 0) *(uint32_t *)at.power = w;
         at.next(p, lane);
     }
@@ -395,13 +324,13 @@ int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, i
     return RWKV7_OK;
 }
 
-cudaError_t mx_launch_rows(const void *kernel, MxRowsParams &p, const LaunchCfg &lc) {
+cudaError_t mx_launch_rows(const void *kernel, MxRowsParams &p, cudaStream_t stream) {
     p.per = p.lines >= MXQ_MANY ? MXQ_LINES : 1;
     const int per = MXQ_THREADS / 32 * p.per;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.lines + (int64_t)per - 1) / per));
     cfg.blockDim = dim3(MXQ_THREADS);
-    cfg.stream = lc.stream;
+    cfg.stream = stream;
     void *args[] = {&p};
     return cudaLaunchKernelExC(&cfg, kernel, args);
 }
@@ -465,7 +394,7 @@ int rwkv7_mx4_quantize(const void *d_x, int32_t dtype, int64_t rows, int64_t col
     MxRowsParams p;
     int rc = mx_rows_check(p, d_x, dtype, rows, cols, ld, d_mx, err_msg);
     if (rc || rows == 0) return rc;
-    return mx_done(err_msg, "quantising", mx_launch_rows(mx_quantize_fn(dtype), p, LaunchCfg{static_cast<cudaStream_t>(cuda_stream), false}));
+    return mx_done(err_msg, "quantising", mx_launch_rows(mx_quantize_fn(dtype), p, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y, int32_t dtype, int64_t ld,
@@ -473,7 +402,7 @@ int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y
     MxRowsParams p;
     int rc = mx_rows_check(p, d_y, dtype, rows, cols, ld, d_mx, err_msg);
     if (rc || rows == 0) return rc;
-    return mx_done(err_msg, "reading back", mx_launch_rows(mx_dequantize_fn(dtype), p, LaunchCfg{static_cast<cudaStream_t>(cuda_stream), false}));
+    return mx_done(err_msg, "reading back", mx_launch_rows(mx_dequantize_fn(dtype), p, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx, int64_t B, const void *d_w_mx, int64_t N,
@@ -493,15 +422,20 @@ int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx
         return mx_fail(err_msg, RWKV7_EINVAL, "the output pointer is not aligned to its type");
     if (((uintptr_t)d_x_mx | (uintptr_t)d_w_mx) & 15u)
         return mx_fail(err_msg, RWKV7_EINVAL, "MXFP4 matrices must be 16-byte aligned");
-    const LaunchCfg lc{static_cast<cudaStream_t>(cuda_stream), false};
-    if (d_x) {
-        MxRowsParams q;
-        int rc = mx_rows_check(q, d_x, x_dtype, B, K, ldx, d_x_mx, err_msg);
-        if (rc) return rc;
-        rc = mx_done(err_msg, "quantising", mx_launch_rows(mx_quantize_fn(x_dtype), q, lc));
-        if (rc) return rc;
-    }
     MxLinearParams p;
+    memset(&p, 0, sizeof p);
+    struct Rows {
+        MxRowsParams q;
+        int type;
+        cudaStream_t stream;
+    } rows;
+    if (d_x) {
+        int rc = mx_rows_check(rows.q, d_x, x_dtype, B, K, ldx, d_x_mx, err_msg);
+        if (rc) return rc;
+        rows.type = x_dtype;
+        rows.stream = static_cast<cudaStream_t>(cuda_stream);
+        p.rows = d_x, p.rtype = x_dtype, p.rvec = rows.q.vec, p.ldr = ldx;
+    }
     p.x = static_cast<const uint8_t *>(d_x_mx);
     p.w = static_cast<const uint8_t *>(d_w_mx);
     p.y = d_y;
@@ -510,7 +444,13 @@ int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx
     p.act = activation;
     p.err = d_err;
     cudaError_t e = cudaSuccess;
-    launch_mx_linear(p, y_dtype, LaunchCfg{lc.stream, d_x != nullptr}, &e);
+    launch_mx_linear(
+        p, y_dtype, static_cast<cudaStream_t>(cuda_stream),
+        [](void *r) {
+            Rows &s = *static_cast<Rows *>(r);
+            return mx_launch_rows(mx_quantize_fn(s.type), s.q, s.stream);
+        },
+        &rows, &e);
     return mx_done(err_msg, "MXFP4 product", e);
 }
 

@@ -46,15 +46,20 @@ enum MxFormat : int { MXFP4 = 0, MXINT8 = 1 };
 // One quantised product y = act(xq wq^T); see launch_mx_linear.
 struct MxLinearParams {
     const uint8_t *x, *w;  // MXFP4 matrices [B][K], [N][K]
+    const void *rows;      // if not null, what x is quantised from: rows of type rtype, ldr apart,
+    int rtype, rvec;       // rvec: on 16-byte (fp32: 32-byte) boundaries
+    int64_t ldr;
     void *y;
     int64_t ldy;
     int B, N, K;
     int act;  // 0 none, 1 relu(.)^2
     uint32_t *err;
 };
-// type: MxType of y.  pdl: the kernel before it on the stream writes x and lets
-// this one start early.
-void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cudaError_t *e);
+// type: MxType of y.  Where p.rows is given and the product is not one that quantises
+// them itself, quantize(ctx) is called first to launch the kernel that writes p.x; the
+// product then starts early, beside it.
+void launch_mx_linear(const MxLinearParams &p, int type, cudaStream_t stream, cudaError_t (*quantize)(void *), void *ctx,
+                      cudaError_t *e);
 
 // The slot pool of a ctx, for saving and loading states (mx_ctx_states).
 struct MxCtxStates {
@@ -137,6 +142,84 @@ __device__ __forceinline__ uint32_t mx_quad_top(const float (&v)[8]) {
     for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
     return max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+}
+
+// Eight neighbouring values of a row as a lane holds them between load and use: in
+// 16-bit types two a word, so that four lines in flight take 16 registers.
+template <int T>
+struct MxElem;
+template <>
+struct MxElem<MX_F32> {
+    using type = float;
+    struct Eight {
+        float v[8];
+    };
+    static __device__ __forceinline__ void load(Eight &u, const float *p) { ld_v8(u.v, p); }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[8]) { st_v8(p, v); }
+    static __device__ __forceinline__ void set(Eight &u, int i, float v) { u.v[i] = v; }
+    static __device__ __forceinline__ uint32_t top(const Eight &u) { return mx_quad_top(u.v); }
+    static __device__ __forceinline__ float up(const Eight &u, int i) { return u.v[i]; }
+    static __device__ __forceinline__ float down(float v) { return v; }
+};
+// 16-bit types.  Their bits without the sign order like their values (infinity and
+// NaN last), as pairs of unsigned halves.
+template <typename E>
+struct MxHalves {
+    using type = E;
+    struct Eight {
+        uint32_t w[4];
+    };
+    static __device__ __forceinline__ void load(Eight &u, const E *p) { *(uint4 *)u.w = *(const uint4 *)p; }
+    static __device__ __forceinline__ void set(Eight &u, int i, E v) { ((E *)u.w)[i] = v; }
+    static __device__ __forceinline__ uint32_t top_bits(const Eight &u) {
+        uint32_t m = __vmaxu2(__vmaxu2(u.w[0] & 0x7FFF7FFFu, u.w[1] & 0x7FFF7FFFu),
+                              __vmaxu2(u.w[2] & 0x7FFF7FFFu, u.w[3] & 0x7FFF7FFFu));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        return max(m >> 16, m & 0xFFFFu);
+    }
+};
+template <>
+struct MxElem<MX_F16> : MxHalves<__half> {
+    static __device__ __forceinline__ uint32_t top(const Eight &u) {
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top_bits(u))));
+    }
+    static __device__ __forceinline__ float up(const Eight &u, int i) { return __half2float(((const __half *)u.w)[i]); }
+    static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ void store(__half *p, const float (&v)[8]) {
+        __half2 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        *(uint4 *)p = *(const uint4 *)h;
+    }
+};
+template <>
+struct MxElem<MX_BF16> : MxHalves<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t top(const Eight &u) { return top_bits(u) << 16; }
+    static __device__ __forceinline__ float up(const Eight &u, int i) {
+        return __uint_as_float(i & 1 ? u.w[i >> 1] & 0xFFFF0000u : u.w[i >> 1] << 16);
+    }
+    static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
+        __nv_bfloat162 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        *(uint4 *)p = *(const uint4 *)h;
+    }
+};
+
+// A block's power and a lane's eight codes of a line (256 columns of a row, eight a
+// lane); lanes 0 and 16 get the word of their half line's four powers.
+template <int T>
+__device__ __forceinline__ uint32_t mx4_line(const typename MxElem<T>::Eight &u, uint32_t &powers) {
+    const uint32_t s = mx_scale<MXFP4>(MxElem<T>::top(u));
+    const float f = mx_inverse(s);  // a block without a number: its codes do not matter
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = MxElem<T>::up(u, i) * f;
+    powers = s | __shfl_down_sync(0xffffffffu, s, 4) << 8;
+    powers |= __shfl_down_sync(0xffffffffu, powers, 8) << 16;
+    return fp4_pack8(v);
 }
 #endif
 

@@ -18,6 +18,9 @@
 //                for the kernel that quantises x
 //   warp 1       per stage: powers from shared into tensor memory (tcgen05.cp, in
 //                order before the products of the same thread), four products
+//   (few rows    x is quantised by the product itself: every CTA's epilogue warps turn
+//                the rows over its columns to codes and powers that stay in shared
+//                memory, while the first weights are on their way)
 //   warps 2-17   the accumulator to registers, then, while the next tile's products
 //                run, activation and y; lane = output, so a warp's store of one token
 //                covers 32 neighbouring outputs
@@ -50,6 +53,7 @@ struct MxLinearArgs {
     int split;        // CTAs of a cluster, which share one tile's column tiles
     int pack;         // y's rows allow stores of two (16-bit types) or four (split) neighbours
     uint32_t stage_bytes;
+    uint32_t xres;    // x quantised here: where in shared memory its records lie; 0: x comes through the ring
     uint32_t ncols;   // tensor memory columns
 };
 
@@ -191,6 +195,41 @@ __device__ __forceinline__ void store4(O *y, int n, int N, bool pack, int act, f
     }
 }
 
+constexpr uint32_t MXL_XREC = MX_SCALE_BYTES + 16 * 128;  // x's record of up to 16 rows x 256 columns in shared memory
+constexpr int MXL_XLINES = 4;                             // lines of x that an epilogue warp quantises, at most
+
+// Epilogue warp `w`'s share of the B x kn lines (a line: 256 columns of a row) from
+// column tile k0 on, into records at xres.
+template <int T>
+__device__ __forceinline__ void quantize_x(const MxLinearParams &p, uint8_t *xres, int k0, int kn, int w, int lane) {
+    using L = MxElem<T>;
+    using E = typename L::type;
+    typename L::Eight u[MXL_XLINES];
+#pragma unroll
+    for (int i = 0; i < MXL_XLINES; ++i) {
+        const int line = w + i * MXL_EPI_WARPS;
+        if (line >= p.B * kn) break;
+        const int k = line / p.B, r = line - k * p.B, c = (k0 + k) * MX_TILE_K + lane * 8;
+        const E *src = (const E *)p.rows + r * p.ldr + c;
+        if (p.rvec && c + 8 <= p.K) {
+            L::load(u[i], src);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) L::set(u[i], j, c + j < p.K ? src[j] : L::down(0.0f));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MXL_XLINES; ++i) {
+        const int line = w + i * MXL_EPI_WARPS;
+        if (line >= p.B * kn) break;
+        const int k = line / p.B, r = line - k * p.B, blk = lane >> 2;
+        uint8_t *rec = xres + k * MXL_XREC;
+        uint32_t powers;
+        *(uint32_t *)(rec + MX_SCALE_BYTES + r * 128 + ((blk ^ (r & 7)) << 4) + (lane & 3) * 4) = mx4_line<T>(u[i], powers);
+        if ((lane & 15) == 0) *(uint32_t *)(rec + (blk >> 2) * 512 + r * 16) = powers;
+    }
+}
+
 // Position in the ring: stage and the parity of its current use.
 struct MxRing {
     int st = 0;
@@ -221,7 +260,7 @@ struct MxTile {
 // uniform over it, and one elected lane issues them.  (Issued under a branch on the
 // lane index, with a division for the ring position, a stage took 1.5 times as long.)
 template <int XC>
-__device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32_t sf0, uint32_t stage_bytes, int S, int kn,
+__device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32_t x0, uint32_t sf0, uint32_t stage_bytes, int S, int kn,
                                            int last, int npad, uint32_t off, MxRing &ring, uint64_t *full, uint64_t *empty,
                                            uint64_t *acc_full, volatile uint32_t *abort_flag) {
     const uint32_t id0 = idesc_mxf4(npad, 0), id1 = idesc_mxf4(npad, 1);
@@ -229,8 +268,9 @@ __device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32
         if (!mbar_wait(&full[ring.st], ring.parity, abort_flag)) return false;
         tc_fence_after();
         const uint32_t sw = ring0 + (uint32_t)ring.st * stage_bytes, sfa = sf0 + (uint32_t)ring.st * MXL_SF;
+        const uint32_t sx = x0 ? x0 + (uint32_t)k * MXL_XREC : sw + MX_TILE_BYTES;
         if (elect_one()) {
-            issue_stage<XC>(tmem, sw, sw + MX_TILE_BYTES, sfa, sfa + 8u, off, id0, id1, k > 0, k + 1 < kn ? 4 : last);
+            issue_stage<XC>(tmem, sw, sx, sfa, sfa + 8u, off, id0, id1, k > 0, k + 1 < kn ? 4 : last);
             mma_commit(&empty[ring.st]);
             if (k + 1 == kn) mma_commit(acc_full);
         }
@@ -243,7 +283,7 @@ __device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32
 template <typename O>
 __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_constant__ MxLinearArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[MXL_MAX_STAGES], empty[MXL_MAX_STAGES], acc_full, acc_empty;
+    __shared__ uint64_t full[MXL_MAX_STAGES], empty[MXL_MAX_STAGES], acc_full, acc_empty, x_ready;
     __shared__ uint32_t tmem_slot, s_abort, s_ok[2];
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -253,7 +293,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
     volatile uint32_t *abort_flag = &s_abort;
 
     auto load_w = [&](const MxTile &t, int k, int st) {
-        mbar_expect_tx(&full[st], MX_TILE_BYTES + MX_SCALE_BYTES * (t.r1 ? 2 : 1) + (uint32_t)t.npad * 128u);
+        const uint32_t xbytes = MX_SCALE_BYTES * (t.r1 ? 2 : 1) + (uint32_t)t.npad * 128u;
+        mbar_expect_tx(&full[st], MX_TILE_BYTES + (a.xres ? 0u : xbytes));
         bulk_g2s(base + st * a.stage_bytes, a.p.w + ((int64_t)t.rt * a.kt + k0 + k) * MX_TILE_BYTES, MX_TILE_BYTES, &full[st]);
     };
     const int npre = min(S, kn);  // stages of the first tile whose weights are requested at once
@@ -264,6 +305,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
         }
         mbar_init(&acc_full, 1);
         mbar_init(&acc_empty, MXL_EPI_WARPS);
+        mbar_init(&x_ready, MXL_EPI_WARPS);
         s_abort = 0u;
         fence_barrier_init();
         const MxTile t(a, first);
@@ -281,6 +323,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
     if (warp == 0) {
         if (lane == 0) {
             auto load_x = [&](const MxTile &t, int k, int st) {
+                if (a.xres) return;
                 // powers of the second record, powers of the first, codes of both
                 uint8_t *to = base + st * a.stage_bytes + MX_TILE_BYTES;
                 const uint8_t *x0 = a.p.x + ((int64_t)(t.b0 / MX_TILE_M) * a.kt + k0 + k) * MX_TILE_BYTES;
@@ -329,6 +372,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
         MxRing ring;
         // a last tile of K % 256 columns: the instructions past them would add zeros
         const int last = min(4, (a.p.K - (k0 + kn - 1) * MX_TILE_K + 63) / 64);
+        const uint32_t x0 = a.xres ? smem_u32(base + a.xres) - MX_SCALE_BYTES : 0u;
+        if (a.xres) ok = mbar_wait(&x_ready, 0u, abort_flag);
         const uint32_t ring0 = smem_u32(base), sf0 = tmem + (uint32_t)a.nt;
         for (int i = first; i < a.tiles && ok; i += step, ++n) {
             const MxTile t(a, i);
@@ -336,8 +381,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
                 ok = false;
                 break;
             }
-            ok = t.r1 ? issue_tile<8>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag)
-                      : issue_tile<4>(tmem, ring0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag);
+            ok = t.r1 ? issue_tile<8>(tmem, ring0, x0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag)
+                      : issue_tile<4>(tmem, ring0, x0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag);
         }
         if (!ok && elect_one()) {
             *abort_flag = 1u;
@@ -348,6 +393,14 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
         }
     } else {
         pdl_wait();  // y may have readers before the kernel this one follows
+        if (a.xres) {
+            if (a.p.rtype == MX_F16) quantize_x<MX_F16>(a.p, base + a.xres, k0, kn, warp - 2, lane);
+            else if (a.p.rtype == MX_BF16) quantize_x<MX_BF16>(a.p, base + a.xres, k0, kn, warp - 2, lane);
+            else quantize_x<MX_F32>(a.p, base + a.xres, k0, kn, warp - 2, lane);
+            fence_proxy_async();  // the tensor cores read it through the other proxy
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x_ready);
+        }
         const int qd = warp & 3, grp = (warp - 2) >> 2, row = qd * 32 + lane;
         float *part = (float *)base;  // split: [npad][128] partial sums, over the ring once it is done with
         int n = 0;
@@ -469,6 +522,10 @@ const MxClusters *max_clusters(const void *fn, cudaError_t *e) {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Column tiles of x that a CTA keeps quantised: 16 leave the ring ten stages.  Quantising
+// in the product takes one launch instead of two.
+constexpr int MXL_XRES = 16;
+
 // Tokens of a tile and CTAs of a cluster: the pair with the least estimate of a CTA's
 // time from its first stage on, in ns.  A stage takes 250 + 0.6 nt (copies, powers and
 // products; measured 260-290 at 16 and 64 tokens, 300 at 128, 390 at 256), a tile's end
@@ -494,7 +551,8 @@ void choose(MxLinearArgs &a, const MxClusters &most) {
 
 }  // namespace
 
-void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cudaError_t *e) {
+void launch_mx_linear(const MxLinearParams &p, int type, cudaStream_t stream, cudaError_t (*quantize)(void *), void *ctx,
+                      cudaError_t *e) {
     const void *fn = type == MX_F32   ? (const void *)mx_linear_kernel<float>
                      : type == MX_F16 ? (const void *)mx_linear_kernel<__half>
                                       : (const void *)mx_linear_kernel<__nv_bfloat16>;
@@ -509,7 +567,18 @@ void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cu
     // Every CTA as many tiles as the one with most.
     const int clusters = a.split > 1 ? a.tiles : ceil_div(a.tiles, ceil_div(a.tiles, most->n[1]));
     a.stage_bytes = MX_TILE_BYTES + 2 * MX_SCALE_BYTES + (uint32_t)a.nt * 128u;
-    a.stages = std::min({MXL_MAX_STAGES, (int)((MXL_SMEM_MAX - 1024) / a.stage_bytes), (512 - a.nt) / (int)MXL_SF});
+    uint32_t smem = MXL_SMEM_MAX - 1024;
+    a.xres = 0;
+    const int kn = ceil_div(a.kt, a.split);
+    if (p.rows && p.B <= 16 && p.B * kn <= MXL_XLINES * MXL_EPI_WARPS && kn <= MXL_XRES) {
+        a.stage_bytes = MX_TILE_BYTES;
+        smem -= (uint32_t)kn * MXL_XREC;
+        a.xres = smem & ~1023u;
+    } else if (p.rows) {
+        *e = quantize(ctx);
+        if (*e != cudaSuccess) return;
+    }
+    a.stages = std::min({MXL_MAX_STAGES, (int)(smem / a.stage_bytes), (512 - a.nt) / (int)MXL_SF});
     a.ncols = 512;
     const int size = type == MX_F32 ? 4 : 2;
     const int neigh = a.split > 1 ? 4 * size : 4;
@@ -520,7 +589,7 @@ void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cu
         cfg.gridDim = dim3((unsigned)(clusters * a.split));
         cfg.blockDim = dim3(MXL_THREADS);
         cfg.dynamicSmemBytes = MXL_SMEM_MAX;
-        cfg.stream = lc.stream;
+        cfg.stream = stream;
         cudaLaunchAttribute at[2];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = (unsigned)a.split;
@@ -528,7 +597,7 @@ void launch_mx_linear(const MxLinearParams &p, int type, const LaunchCfg &lc, cu
         at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
-        cfg.numAttrs = lc.pdl ? 2 : 1;
+        cfg.numAttrs = p.rows && !a.xres ? 2 : 1;  // beside the kernel that quantises x
         void *args[] = {&a};
         r = cudaLaunchKernelExC(&cfg, fn, args);
     }

@@ -38,10 +38,9 @@ def _err_word(dev: int) -> torch.Tensor:
     return w
 
 
-def _call(name: str, dev: int, *args):
-    """The library's `name`(*args, stream, &message) on the current stream of device
-    `dev`, with it current."""
-    fn = getattr(load_library(), name)
+def _call(fn, dev: int, *args):
+    """The library's fn(*args, stream, &message) on the current stream of device `dev`,
+    with it current."""
     msg = C.c_char_p()
     if dev == _current_device():
         rc = fn(*args, _raw_stream(dev), C.byref(msg))
@@ -120,14 +119,18 @@ class MX4Matrix:
             rows, cols, ld, code = _rows(out, "out")
             if rows != self.rows or cols != self.cols or out.get_device() != self.data.get_device():
                 raise ValueError("out must have the matrix's shape and device")
-        _call("rwkv7_mx4_dequantize", out.get_device(), self.data.data_ptr(), rows, cols, out.data_ptr(),
+        _call(load_library().rwkv7_mx4_dequantize, out.get_device(), self.data.data_ptr(), rows, cols, out.data_ptr(),
               code, ld)
         return out
 
 
 def mx4_empty(rows: int, cols: int, device) -> MX4Matrix:
     """An MXFP4 matrix whose values are not set yet."""
-    return MX4Matrix(torch.empty(_bytes(rows, cols), dtype=torch.uint8, device=device), rows, cols)
+    m = MX4Matrix.__new__(MX4Matrix)  # (its checks hold by construction, but for the device)
+    m.data, m.rows, m.cols = torch.empty(_bytes(rows, cols), dtype=torch.uint8, device=device), rows, cols
+    if not m.data.is_cuda:
+        raise TypeError("an MXFP4 matrix lies on a CUDA device")
+    return m
 
 
 def mx4_quantize(x, out: MX4Matrix | None = None) -> MX4Matrix:
@@ -138,7 +141,7 @@ def mx4_quantize(x, out: MX4Matrix | None = None) -> MX4Matrix:
         out = mx4_empty(rows, cols, x.device)
     elif out.shape != (rows, cols) or out.data.device != x.device:
         raise ValueError("out must have x's shape and device")
-    _call("rwkv7_mx4_quantize", x.get_device(), x.data_ptr(), code, rows, cols, ld, out.data.data_ptr())
+    _call(load_library().rwkv7_mx4_quantize, x.get_device(), x.data_ptr(), code, rows, cols, ld, out.data.data_ptr())
     return out
 
 
@@ -178,7 +181,7 @@ def mx4_linear(x, w: MX4Matrix, out=None, out_dtype=None, activation=None):
         rows, cols, ldy, out_code = _rows(out, "out")
         if rows != B or cols != N or out.get_device() != dev:
             raise ValueError(f"out must be [{B}, {N}] on cuda:{dev}")
-    _call("rwkv7_mx4_linear", dev, src, code, ldx, data.data_ptr(), B, w.data.data_ptr(), N, K, out.data_ptr(), out_code,
+    _call(load_library().rwkv7_mx4_linear, dev, src, code, ldx, data.data_ptr(), B, w.data.data_ptr(), N, K, out.data_ptr(), out_code,
           ldy, act, _err_word(dev).data_ptr())
     return out
 
@@ -225,7 +228,7 @@ class StateCache:
             raise TypeError("a state cache lies on a CUDA device")
         self.err = torch.zeros(1, dtype=torch.int32, device=self.data.device)
 
-    def _states(self, name, states, slots, entries):
+    def _states(self, fn, states, slots, entries):
         wkv, att, ffn = states
         dev, L, H = self.data.device, self.n_layer, self.n_head
         for what, t in (("wkv", wkv), ("shift_att", att), ("shift_ffn", ffn)):
@@ -237,17 +240,17 @@ class StateCache:
         if wkv.shape != (L, n_slots, H, 64, 64) or att.shape != (L, n_slots, 64 * H) or ffn.shape != att.shape:
             raise ValueError(f"states must be wkv [{L}, slots, {H}, 64, 64] and two token shifts [{L}, slots, {64 * H}]")
         n = _pair_count(slots, entries, dev)
-        _call(name, dev.index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
+        _call(fn, dev.index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
               entries.data_ptr(), n, self.data.data_ptr(), self.n_entries, self.format, self.err.data_ptr())
 
     def save(self, states, slots, entries):
         """Keep the states of `slots` in `entries` (rwkv7_states_save).  states:
         (wkv [L, n_slots, H, 64, 64], shift_att, shift_ffn [L, n_slots, 64 H])."""
-        self._states("rwkv7_states_save", states, slots, entries)
+        self._states(load_library().rwkv7_states_save, states, slots, entries)
 
     def load(self, states, entries, slots):
         """Put the kept states of `entries` into `slots` (rwkv7_states_load)."""
-        self._states("rwkv7_states_load", states, slots, entries)
+        self._states(load_library().rwkv7_states_load, states, slots, entries)
 
     def check(self):
         """Wait for the stream and raise if a save or load had a bad or repeated index."""

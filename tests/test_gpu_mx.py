@@ -493,3 +493,28 @@ def test_example_runs():
     r = microscaled.main(["--shape", "tiny", "--slots", "3", "--prefix", "40"])
     assert 0 < r["mxint8"] < 0.01 and r["mxint8"] < r["mxfp4"] < 0.35
     assert 0 < r["head"] < 0.35 and 0 < r["channel mix"] < 0.6
+
+
+@pytest.mark.parametrize("B,N,K", [(1, 300, 1), (1, 70, 5000), (2, 2560, 2560), (3, 129, 4100), (5, 200, 3333), (7, 96, 2048),
+                                   (9, 1000, 700), (16, 640, 1024), (16, 640, 1100), (16, 20000, 1024), (16, 20000, 1300),
+                                   (4, 20000, 4096), (4, 20000, 4200)])
+def test_product_of_few_rows_quantised_on_the_way(B, N, K):
+    """Up to sixteen rows go through the product's own quantisation or through the
+    kernel before it, as their length has it: to the same bits."""
+    g = cpu(B + N + K)
+    w = rd.mx4_quantize((torch.randn(N, K, generator=g) * 0.05).cuda())
+    for dt in TYPES.values():
+        wide = (torch.randn(B, K + 3, generator=g) * torch.exp(torch.randn(K + 3, generator=g))).to(dt).cuda()
+        for x in (wide[:, :K].contiguous(), wide[:, 3:]):  # on the 16-byte grid (where K is) and off it
+            y = rd.mx4_linear(x, w, out_dtype=torch.float32)
+            rd.mx4_check()
+            assert torch.equal(y, rd.mx4_linear(rd.mx4_quantize(x), w))
+    check_product(B, N, K, "bf16", "fp32", None)
+    check_product(B, N, K, "fp32", "fp16", "relu2", strided=True)
+
+
+def test_few_rows_keep_no_number_to_their_block():
+    x = torch.randn(3, 300, generator=cpu(5))
+    x[1, 290], x[2, 0] = float("inf"), float("nan")
+    y = rd.mx4_linear(x.half().cuda(), rd.mx4_quantize(torch.randn(140, 300, generator=cpu(6)).cuda()))
+    assert bool(torch.isnan(y[1:]).all()) and bool(torch.isfinite(y[0]).all())
