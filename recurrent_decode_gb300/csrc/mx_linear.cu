@@ -81,6 +81,21 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int N, int half) {
     return 1u << 7 | 1u << 10 | (uint32_t)(N >> 3) << 17 | 1u << 23 | 1u << 27 | (uint32_t)half << 5 | (uint32_t)half << 30;
 }
 
+// 32 lanes x 16 columns on their way to v, which holds them after tmem_wait.
+__device__ __forceinline__ void tmem_ask16(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+#define MXL_16(v) "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), \
+                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+__device__ __forceinline__ void tmem_wait(float (&v)[4][16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : MXL_16(v[0]), MXL_16(v[1]), MXL_16(v[2]), MXL_16(v[3])::"memory");
+}
+#undef MXL_16
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
@@ -284,7 +299,7 @@ template <typename O>
 __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_constant__ MxLinearArgs a) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[MXL_MAX_STAGES], empty[MXL_MAX_STAGES], acc_full, acc_empty, x_ready;
-    __shared__ uint32_t tmem_slot, s_abort, s_ok[2];
+    __shared__ uint32_t tmem_slot, s_abort;
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = a.stages, split = a.split;
@@ -406,23 +421,22 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
         int n = 0;
         for (int i = first; i < a.tiles; i += step, ++n) {
             const MxTile t(a, i);
-            if (threadIdx.x == 64) {
-                s_ok[n & 1] = mbar_wait(&acc_full, (uint32_t)n & 1u, abort_flag) ? 1u : 0u;
-                if (!s_ok[n & 1]) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full, (uint32_t)n & 1u, abort_flag))) {
+                if (lane == 0) {
                     *abort_flag = 1u;
                     atomicOr(a.p.err, ERR_TIMEOUT);
                 }
+                break;
             }
-            named_bar(1, MXL_EPI_THREADS);
-            if (!s_ok[n & 1]) break;
             tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(qd * 32) << 16);
-            float v[MXL_CHUNKS][16];
+            // All of the accumulator is asked for before any of it is waited for: until the
+            // registers have it the next tile's products wait.
+            const uint32_t acc = tmem + ((uint32_t)(qd * 32) << 16) + (uint32_t)(grp * 16);
+            float v[MXL_CHUNKS][16] = {};
 #pragma unroll
-            for (int h = 0; h < MXL_CHUNKS; ++h) {
-                const int c = (h * (MXL_EPI_WARPS / 4) + grp) * 16;
-                if (c < t.npad) tmem_ld16(acc + (uint32_t)c, v[h]);
-            }
+            for (int h = 0; h < MXL_CHUNKS; ++h)
+                if ((h * (MXL_EPI_WARPS / 4) + grp) * 16 < t.npad) tmem_ask16(acc + (uint32_t)(h * (MXL_EPI_WARPS / 4) * 16), v[h]);
+            tmem_wait(v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty);
