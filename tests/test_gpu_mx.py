@@ -225,7 +225,7 @@ def test_product_keeps_no_number_to_its_row_and_column(B):
 
 def test_zero_rows_give_zero():
     x = torch.zeros(9, 200, device="cuda")
-    w = rd.mx4_quantize(torch.randn(64, 200, device="cuda"))
+    w = rd.mx4_quantize(torch.randn(64, 200, generator=cpu(11)).cuda())
     assert bool((rd.mx4_linear(x, w) == 0).all())
     w = rd.mx4_quantize(torch.zeros(64, 200, device="cuda"))
     assert bool((rd.mx4_linear(torch.ones(9, 200, device="cuda"), w) == 0).all())
@@ -433,7 +433,7 @@ def test_slots_of_a_context(fmt):
     ctx.slots_save(cache, ints(0, 1), ints(2, 0))
     for k in (2, 3):  # draws that the load has to make undone
         ctx.set_sampling(k, temperature=1.0, top_p=0.9, seed=5)
-    logits = torch.randn(2, dims.vocab, device="cuda")
+    logits = torch.randn(2, dims.vocab, generator=cpu(3)).cuda()
     first, second = ints(0, 0), ints(0, 0)
     ctx.sample_batch(ints(2, 3), logits, first)
     ctx.slots_load(cache, ints(2, 0), ints(3, 2))
@@ -518,3 +518,45 @@ def test_few_rows_keep_no_number_to_their_block():
     x[1, 290], x[2, 0] = float("inf"), float("nan")
     y = rd.mx4_linear(x.half().cuda(), rd.mx4_quantize(torch.randn(140, 300, generator=cpu(6)).cuda()))
     assert bool(torch.isnan(y[1:]).all()) and bool(torch.isfinite(y[0]).all())
+
+
+# ------------------------------------------------------------------ far places
+def test_matrix_past_32_bits():
+    """Rows past 2^32 elements, codes past 2^32 bytes: the last rows of 70,000 x 131,072
+    come back as those of a small matrix do."""
+    R, K = 70000, 131072
+    x = torch.empty(R, K, dtype=torch.bfloat16, device="cuda")
+    x[:64] = 1.0
+    x[-130:] = torch.randn(130, K, generator=cpu(1)).cuda()
+    m = rd.mx4_quantize(x)
+    assert m.data.numel() > 1 << 32
+    small = rd.mx4_quantize(x[-130:])
+    want = small.dequantize(torch.bfloat16)
+    tail = x[-130:].clone()
+    del x
+    y = m.dequantize(torch.bfloat16)
+    assert torch.equal(y[-130:], want) and bool((y[:64] == 1).all())
+    del y
+    got = rd.mx4_linear(tail[:3, :], m, out_dtype=torch.float32)[:, -130:]
+    rd.mx4_check()
+    v = small.dequantize().double().cpu().numpy()
+    want, off = product(v[:3], v, None, torch.float32)
+    assert (np.abs(got.double().cpu().numpy() - want) <= off).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxint8", "mxfp4"])
+def test_entries_and_slots_past_32_bits(fmt):
+    """A pool and a cache of more than 2^32 bytes: the last slots and entries."""
+    L, H, n = 4, 64, 1100  # 4.6 GB of states a layer
+    cache = rd.StateCache(L, H, (1 << 32) // rd.StateCache(L, H, 1, fmt).entry_bytes + 2, fmt)
+    st = (torch.zeros(L, n, H, 64, 64, device="cuda"), torch.zeros(L, n, 64 * H, device="cuda"), torch.zeros(L, n, 64 * H, device="cuda"))
+    st[0][:, n - 1] = torch.randn(L, H, 64, 64, generator=cpu(2)).cuda()
+    st[1][:, n - 1], st[2][:, n - 1] = 3.0, 4.0
+    last = cache.n_entries - 1
+    cache.save(st, ints(n - 1), ints(last))
+    cache.load(st, ints(last, last), ints(0, n - 2))
+    cache.check()
+    want = nearest(st[0][-1, n - 1, -1].double().cpu().numpy(), fmt)
+    same(st[0][-1, n - 2, -1], want)
+    same(st[0][-1, 0, -1], want)
+    assert bool((st[1][:, n - 2] == 3).all()) and bool((st[2][:, 0] == 4).all()) and bool((st[0][:, 1:n - 2] == 0).all())
