@@ -1,9 +1,17 @@
 // mx.cu -- MXFP4 quantisation of rows and its inverse, and slot states saved to
 // and loaded from a cache of MXINT8 or MXFP4 entries (formats: mx.cuh).
 //
-// All four kernels move each value once and do a handful of operations on it, so
-// HBM bounds them; eight neighbouring values belong to one lane and a block of 32
-// to four, whose largest value takes two shuffles.
+// All four kernels move each value once and do a handful of operations on it; eight
+// neighbouring values belong to one lane and a block of 32 to four, whose largest
+// value takes two shuffles.  Measured against the 6.8 TB/s of a plain copy:
+//   states   sixteen of the 2.9B shape saved and loaded as MXINT8, 885 MB: 134 us, 6.6
+//            TB/s; one 7.2B state loaded into 48 slots, 1.7 GB: 259 us, 6.6 TB/s.
+//            Memory bounds them.  Stored 16 bytes a lane instead of 32 (two halves of
+//            each sector at different times) the load took 341 us.
+//   rows     4096 x 16384 bf16 to MXFP4, 170 MB: 28 us, 6.1 TB/s; back, 26.5 us, 6.4
+//            TB/s.  Addresses worked out line by line took 34 us (issue slots 74 %
+//            busy), one line a warp instead of four 59 and 45 us; for 64 x 2560 four
+//            lines a warp took 2.3 us instead of 1.6.
 #include <cstdio>
 #include <cstring>
 
@@ -23,7 +31,9 @@ struct MxRowsParams {
 
 constexpr int MXQ_THREADS = 256;
 constexpr int MXQ_LINES = 4;  // lines of a warp at most, their loads issued together
-constexpr int MXQ_MANY = 152 * 8 * 8;  // from here on (eight warps on each SM eight times over) a warp takes them all
+// From here on a warp takes them all: 64 warps for each SM are there without it, and
+// with fewer lines one a warp spreads them over more SMs.
+constexpr int MXQ_MANY = 152 * 64;
 
 // Where a line lies: its values, a lane's four bytes of codes, the word of a half
 // line's powers.  Walks on line by line.
@@ -55,8 +65,14 @@ struct MxLine {
             row(p, lane);
         }
     }
+    // whether `n` lines from here on are whole ones of one row on the 16-byte grid
+    __device__ __forceinline__ bool plain(const MxRowsParams &p, int n) const {
+        return n == MXQ_LINES && p.vec && (int64_t)(t + MXQ_LINES) * MX_TILE_K <= p.cols;
+    }
     // how many of the line's 256 columns the matrix has
-    __device__ __forceinline__ int cols(const MxRowsParams &p) const { return (int)min((int64_t)MX_TILE_K, p.cols - (int64_t)t * MX_TILE_K); }
+    __device__ __forceinline__ int cols(const MxRowsParams &p) const {
+        return (int)min((int64_t)MX_TILE_K, p.cols - (int64_t)t * MX_TILE_K);
+    }
 };
 
 // A warp takes p.per consecutive lines (a line: 256 columns of a row), eight values a
@@ -74,6 +90,17 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_quantize_kernel(const MxRowsP
     if (n <= 0) return;
     typename L::Eight u[MXQ_LINES];
     MxLine<E> at(p, first, lane);
+    if (at.plain(p, n)) {  // the usual case, at fixed distances
+#pragma unroll
+        for (int l = 0; l < MXQ_LINES; ++l) L::load(u[l], at.x + l * MX_TILE_K + lane * 8);
+#pragma unroll
+        for (int l = 0; l < MXQ_LINES; ++l) {
+            uint32_t w;
+            *(uint32_t *)(at.code + l * MX_TILE_BYTES) = mx4_line<T>(u[l], w);
+            if ((lane & 15) == 0) *(uint32_t *)(at.power + l * MX_TILE_BYTES) = w;
+        }
+        return;
+    }
     const MxLine<E> start = at;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
@@ -121,6 +148,20 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRow
     if (n <= 0) return;
     uint32_t code[MXQ_LINES], s[MXQ_LINES];
     MxLine<E> at(p, first, lane);
+    if (at.plain(p, n)) {  // the usual case, at fixed distances
+#pragma unroll
+        for (int l = 0; l < MXQ_LINES; ++l) {
+            code[l] = *(const uint32_t *)(at.code + l * MX_TILE_BYTES);
+            s[l] = at.power[l * MX_TILE_BYTES + ((lane >> 2) & 3)];
+        }
+#pragma unroll
+        for (int l = 0; l < MXQ_LINES; ++l) {
+            float v[8];
+            mx4_values(code[l], s[l], v);
+            L::store(at.x + l * MX_TILE_K + lane * 8, v);
+        }
+        return;
+    }
     const MxLine<E> start = at;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
@@ -134,10 +175,7 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRow
     for (int l = 0; l < MXQ_LINES; ++l) {
         if (l >= n) break;
         float v[8];
-        fp4_unpack8(code[l], v);
-        const float f = s[l] == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s[l]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= f;
+        mx4_values(code[l], s[l], v);
         const int cols = at.cols(p);
         if (p.vec && lane * 8 + 8 <= cols) {
             L::store(at.x + lane * 8, v);
@@ -182,7 +220,9 @@ struct MxStateParams {
     int V;
 };
 
-__host__ __device__ constexpr int64_t mx_codes(int64_t heads, int fmt) { return heads * (fmt == MXINT8 ? MX_HEAD : MX_HEAD / 2); }
+__host__ __device__ constexpr int64_t mx_codes(int64_t heads, int fmt) {
+    return heads * (fmt == MXINT8 ? MX_HEAD : MX_HEAD / 2);
+}
 
 // Whether this CTA's pair i is one to carry out: both indices in range, and no
 // earlier pair with the same target (one of two copies into the same place would
@@ -298,7 +338,9 @@ int mx_done(const char **err_msg, const char *what, cudaError_t e) {
     if (err_msg) *err_msg = g_mx_msg;
     return RWKV7_ECUDA;
 }
-bool mx_size_ok(int64_t rows, int64_t cols) { return rows >= 0 && cols >= 1 && rows <= RWKV7_MX_MAX_DIM && cols <= RWKV7_MX_MAX_DIM; }
+bool mx_size_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && cols >= 1 && rows <= RWKV7_MX_MAX_DIM && cols <= RWKV7_MX_MAX_DIM;
+}
 
 int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, const void *mx,
                   const char **err_msg) {

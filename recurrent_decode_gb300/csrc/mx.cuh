@@ -6,12 +6,12 @@
 //           s - 127 is the least e >= -127 with max |x| <= 6 * 2^e
 //   MXINT8  8 bits a value, q / 64 with q in -127 .. 127;
 //           s - 127 is the least e >= -126 with max |x| <= 127/64 * 2^e
-//           (at most 127: fp32 values within 2^-7 of the type's end are cut to it)
+//           (at most 127: values in the last 128th of fp32's range are cut to it)
 //
-// Formats and the byte's meaning are those of the Open Compute Project's
-// microscaling specification (v1.0).  It leaves the choice of the power open; the least one that cuts off
-// no value is taken here, so the largest value of a block, which carries most of
-// a sum, is never off by more than half a step.  x * 2^-e is exact in fp32 (or
+// Formats and the byte's meaning are those of the Open Compute Project's microscaling
+// specification (v1.0).  It leaves the choice of the power open; the least one that
+// cuts off no value is taken here, so the largest value of a block, which carries most
+// of a sum, is never off by more than half a step.  x * 2^-e is exact in fp32 (or
 // below every threshold of the grid), so a code depends on the value alone: to
 // the nearest grid point, ties to the even code.  A block that holds an infinity
 // or NaN gets s = 255 and reads back as NaN.
@@ -123,6 +123,13 @@ __device__ __forceinline__ void fp4_unpack8(uint32_t r, float (&v)[8]) {
         v[2 * i + 1] = f.y;
     }
 }
+// The values of eight codes of a block of power s.
+__device__ __forceinline__ void mx4_values(uint32_t code, uint32_t s, float (&v)[8]) {
+    fp4_unpack8(code, v);
+    const float f = s == 255u ? __uint_as_float(0x7FC00000u) : mx_power(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= f;
+}
 // Eight floats at a 32-byte aligned address, by one access.
 __device__ __forceinline__ void ld_v8(float (&v)[8], const float *p) {
     asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -184,7 +191,9 @@ struct MxElem<MX_F16> : MxHalves<__half> {
     static __device__ __forceinline__ uint32_t top(const Eight &u) {
         return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top_bits(u))));
     }
-    static __device__ __forceinline__ float up(const Eight &u, int i) { return __half2float(((const __half *)u.w)[i]); }
+    static __device__ __forceinline__ float up(const Eight &u, int i) {
+        return __half2float(((const __half *)u.w)[i]);
+    }
     static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
     static __device__ __forceinline__ void store(__half *p, const float (&v)[8]) {
         __half2 h[4];

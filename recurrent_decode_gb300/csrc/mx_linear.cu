@@ -18,14 +18,27 @@
 //                for the kernel that quantises x
 //   warp 1       per stage: powers from shared into tensor memory (tcgen05.cp, in
 //                order before the products of the same thread), four products
-//   (few rows    x is quantised by the product itself: every CTA's epilogue warps turn
-//                the rows over its columns to codes and powers that stay in shared
-//                memory, while the first weights are on their way)
 //   warps 2-17   the accumulator to registers, then, while the next tile's products
 //                run, activation and y; lane = output, so a warp's store of one token
 //                covers 32 neighbouring outputs
+// Up to 16 rows of x of moderate length are quantised by these warps of every CTA
+// themselves, into shared memory where they stay, while the first weights are on
+// their way.
+//
 // Each stage has columns of its own for its powers: they are overwritten only
-// after the commit that also frees the stage's shared memory.
+// after the commit that also frees the stage's shared memory.  A CTA takes all of
+// tensor memory; its 226 KB of shared memory keep any other CTA that uses tensor
+// memory off the SM, so none waits for columns that a waiting CTA holds.
+//
+// What bounds it (2.07 GHz): an SM takes in 64 bytes a clock, 132 GB/s, which for a
+// stage of 128 outputs x 256 tokens x 256 columns (51 KB) is 388 ns; its products
+// alone take 314, its powers 40 more; 391 measured, 5.1 PFLOP/s over a 7.2B prefill
+// key (4096 x 4096 x 16384, 108 us, 1365 W of 1400 when kept up).  128 tokens a tile
+// (36 KB a stage for half the products) took 160 us there.  A single row of the 2.9B head streams 89 MB of weights in 18.6 us: 13.2 at the
+// memory's rate, the rest before the first bytes arrive (2.3 us) and after the last.
+// A tile that four CTAs share spends 4 us on its partial sums, 2.6 of them because
+// they lie on other SMs (256 tokens; storing them there instead of fetching them took
+// longer).
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -48,7 +61,8 @@ struct MxLinearArgs {
     MxLinearParams p;
     int kt;           // column tiles
     int nt;           // tokens of a full tile, a multiple of 16
-    int rtiles, tiles;  // tiles of outputs; all tiles, outputs fastest
+    int rtiles;       // tiles along the outputs
+    int tiles;        // all tiles, outputs fastest
     int stages;       // of the ring
     int split;        // CTAs of a cluster, which share one tile's column tiles
     int pack;         // y's rows allow stores of two (16-bit types) or four (split) neighbours
@@ -171,7 +185,8 @@ struct MxOut<__nv_bfloat16> {
 // n's in v.  16-bit types: neighbouring lanes trade halves, so that each stores two
 // outputs of every other token.
 template <typename O>
-__device__ __forceinline__ void store16(O *y, int64_t ldy, int c, int rows, int n, int N, bool pack, int act, float (&v)[16]) {
+__device__ __forceinline__ void store16(O *y, int64_t ldy, int c, int rows, int n, int N, bool pack, int act,
+                                        float (&v)[16]) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = mx_act(v[j], act);
     if constexpr (sizeof(O) == 2) {
@@ -201,8 +216,10 @@ template <typename O>
 __device__ __forceinline__ void store4(O *y, int n, int N, bool pack, int act, float4 s) {
     const float v[4] = {mx_act(s.x, act), mx_act(s.y, act), mx_act(s.z, act), mx_act(s.w, act)};
     if (pack && n + 3 < N) {
-        if constexpr (sizeof(O) == 2) *(uint2 *)(y + n) = make_uint2(MxOut<O>::two(v[0], v[1]), MxOut<O>::two(v[2], v[3]));
-        else *(float4 *)(y + n) = make_float4(v[0], v[1], v[2], v[3]);
+        if constexpr (sizeof(O) == 2)
+            *(uint2 *)(y + n) = make_uint2(MxOut<O>::two(v[0], v[1]), MxOut<O>::two(v[2], v[3]));
+        else
+            *(float4 *)(y + n) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -210,7 +227,7 @@ __device__ __forceinline__ void store4(O *y, int n, int N, bool pack, int act, f
     }
 }
 
-constexpr uint32_t MXL_XREC = MX_SCALE_BYTES + 16 * 128;  // x's record of up to 16 rows x 256 columns in shared memory
+constexpr uint32_t MXL_XREC = MX_SCALE_BYTES + 16 * 128;  // x's record of up to 16 rows x 256 columns
 constexpr int MXL_XLINES = 4;                             // lines of x that an epilogue warp quantises, at most
 
 // Epilogue warp `w`'s share of the B x kn lines (a line: 256 columns of a row) from
@@ -275,10 +292,10 @@ struct MxTile {
 // uniform over it, and one elected lane issues them.  (Issued under a branch on the
 // lane index, with a division for the ring position, a stage took 1.5 times as long.)
 template <int XC>
-__device__ __forceinline__ bool issue_tile(uint32_t tmem, uint32_t ring0, uint32_t x0, uint32_t sf0, uint32_t stage_bytes, int S, int kn,
-                                           int last, int npad, uint32_t off, MxRing &ring, uint64_t *full, uint64_t *empty,
-                                           uint64_t *acc_full, volatile uint32_t *abort_flag) {
-    const uint32_t id0 = idesc_mxf4(npad, 0), id1 = idesc_mxf4(npad, 1);
+__device__ __forceinline__ bool issue_tile(const MxTile &t, uint32_t tmem, uint32_t ring0, uint32_t x0, uint32_t sf0,
+                                           uint32_t stage_bytes, int S, int kn, int last, MxRing &ring, uint64_t *full,
+                                           uint64_t *empty, uint64_t *acc_full, volatile uint32_t *abort_flag) {
+    const uint32_t id0 = idesc_mxf4(t.npad, 0), id1 = idesc_mxf4(t.npad, 1), off = (uint32_t)t.off >> 5;
     for (int k = 0; k < kn; ++k) {
         if (!mbar_wait(&full[ring.st], ring.parity, abort_flag)) return false;
         tc_fence_after();
@@ -310,7 +327,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
     auto load_w = [&](const MxTile &t, int k, int st) {
         const uint32_t xbytes = MX_SCALE_BYTES * (t.r1 ? 2 : 1) + (uint32_t)t.npad * 128u;
         mbar_expect_tx(&full[st], MX_TILE_BYTES + (a.xres ? 0u : xbytes));
-        bulk_g2s(base + st * a.stage_bytes, a.p.w + ((int64_t)t.rt * a.kt + k0 + k) * MX_TILE_BYTES, MX_TILE_BYTES, &full[st]);
+        bulk_g2s(base + st * a.stage_bytes, a.p.w + ((int64_t)t.rt * a.kt + k0 + k) * MX_TILE_BYTES, MX_TILE_BYTES,
+                 &full[st]);
     };
     const int npre = min(S, kn);  // stages of the first tile whose weights are requested at once
     if (threadIdx.x == 0) {
@@ -396,8 +414,10 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
                 ok = false;
                 break;
             }
-            ok = t.r1 ? issue_tile<8>(tmem, ring0, x0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag)
-                      : issue_tile<4>(tmem, ring0, x0, sf0, a.stage_bytes, S, kn, last, t.npad, (uint32_t)t.off >> 5, ring, full, empty, &acc_full, abort_flag);
+            ok = t.r1 ? issue_tile<8>(t, tmem, ring0, x0, sf0, a.stage_bytes, S, kn, last, ring, full, empty, &acc_full,
+                                      abort_flag)
+                      : issue_tile<4>(t, tmem, ring0, x0, sf0, a.stage_bytes, S, kn, last, ring, full, empty, &acc_full,
+                                      abort_flag);
         }
         if (!ok && elect_one()) {
             *abort_flag = 1u;
@@ -435,7 +455,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx_linear_kernel(const __grid_
             float v[MXL_CHUNKS][16] = {};
 #pragma unroll
             for (int h = 0; h < MXL_CHUNKS; ++h)
-                if ((h * (MXL_EPI_WARPS / 4) + grp) * 16 < t.npad) tmem_ask16(acc + (uint32_t)(h * (MXL_EPI_WARPS / 4) * 16), v[h]);
+                if ((h * (MXL_EPI_WARPS / 4) + grp) * 16 < t.npad)
+                    tmem_ask16(acc + (uint32_t)(h * (MXL_EPI_WARPS / 4) * 16), v[h]);
             tmem_wait(v);
             tc_fence_before();
             __syncwarp();
@@ -511,6 +532,7 @@ const MxClusters *max_clusters(const void *fn, cudaError_t *e) {
     }
     if (done[dev].load(std::memory_order_acquire)) return &known[dev];
     std::lock_guard<std::mutex> lk(mu);
+    if (done[dev].load(std::memory_order_acquire)) return &known[dev];
     *e = ensure_smem_attr(fn, (int)MXL_SMEM_MAX);
     for (int s = 1; s <= MXL_MAX_SPLIT && *e == cudaSuccess; ++s) {
         cudaLaunchConfig_t cfg = {};

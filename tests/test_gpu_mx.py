@@ -65,6 +65,20 @@ def test_rows_at_any_address(offset):
     assert bool((room == 9.0).all())  # nothing else was written
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(4000, 1280), (2500, 1300), (10001, 256), (3000, 1024)])
+def test_many_rows_as_few(rows, cols, dtype):
+    """Matrices large enough for several lines a warp, whole and ragged, against the
+    reference on some rows and against the same rows quantised a few at a time."""
+    x = (torch.randn(rows, cols, generator=cpu(rows)) * 5).to(TYPES[dtype])
+    x[7, 9] = float("nan")
+    y = rd.mx4_quantize(x.cuda()).dequantize(TYPES[dtype])
+    some = [0, 1, 2, 3, 7, 8, 127, 128, 129, rows // 2, rows - 2, rows - 1]
+    same(y[some], nearest(x[some].double().numpy(), "mxfp4"))
+    parts = [rd.mx4_quantize(x[a:a + 800].cuda()).dequantize(TYPES[dtype]) for a in range(0, rows, 800)]
+    assert torch.equal(torch.nan_to_num(y, 77.0), torch.nan_to_num(torch.cat(parts), 77.0))
+
+
 def test_ties_and_signs():
     v = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]
     row = torch.tensor(v + [-t for t in v] + [0.0, -0.0] + [0.2499, 0.2501, 4.999, 5.001] + [0.0] * 10)
