@@ -30,12 +30,15 @@
 // tensor memory; its 226 KB of shared memory keep any other CTA that uses tensor
 // memory off the SM, so none waits for columns that a waiting CTA holds.
 //
-// What bounds it (2.07 GHz): an SM takes in 64 bytes a clock, 132 GB/s, which for a
-// stage of 128 outputs x 256 tokens x 256 columns (51 KB) is 388 ns; its products
-// alone take 314, its powers 40 more; 391 measured, 5.1 PFLOP/s over a 7.2B prefill
-// key (4096 x 4096 x 16384, 108 us, 1365 W of 1400 when kept up).  128 tokens a tile
-// (36 KB a stage for half the products) took 160 us there.  A single row of the 2.9B head streams 89 MB of weights in 18.6 us: 13.2 at the
-// memory's rate, the rest before the first bytes arrive (2.3 us) and after the last.
+// What bounds it (2.07 GHz): a stage of 128 outputs x 256 tokens x 256 columns takes
+// 372 ns; its copies alone (52 KB out of L2 on every SM, 24 TB/s) take 332, its
+// products and powers alone 342 (253 issued back to back; waits for stages that spin
+// without ever looking at the clock give 303, but 363 together with the copies), so
+// both sides are near their limits.  5.1 PFLOP/s over a 7.2B prefill key
+// (4096 x 4096 x 16384, 108 us, 1365 W of 1400 when kept up).  128 tokens a tile (36 KB
+// a stage for half the products) took 160 us there.  A single row of the 2.9B head
+// streams 89 MB of weights in 18.6 us: 13.2 at the memory's rate, the rest before the
+// first bytes arrive (2.3 us) and after the last.
 // A tile that four CTAs share spends 4 us on its partial sums, 2.6 of them because
 // they lie on other SMs (256 tokens; storing them there instead of fetching them took
 // longer).
@@ -296,12 +299,13 @@ __device__ __forceinline__ bool issue_tile(const MxTile &t, uint32_t tmem, uint3
                                            uint32_t stage_bytes, int S, int kn, int last, MxRing &ring, uint64_t *full,
                                            uint64_t *empty, uint64_t *acc_full, volatile uint32_t *abort_flag) {
     const uint32_t id0 = idesc_mxf4(t.npad, 0), id1 = idesc_mxf4(t.npad, 1), off = (uint32_t)t.off >> 5;
+    const bool leader = elect_one();
     for (int k = 0; k < kn; ++k) {
         if (!mbar_wait(&full[ring.st], ring.parity, abort_flag)) return false;
         tc_fence_after();
         const uint32_t sw = ring0 + (uint32_t)ring.st * stage_bytes, sfa = sf0 + (uint32_t)ring.st * MXL_SF;
         const uint32_t sx = x0 ? x0 + (uint32_t)k * MXL_XREC : sw + MX_TILE_BYTES;
-        if (elect_one()) {
+        if (leader) {
             issue_stage<XC>(tmem, sw, sx, sfa, sfa + 8u, off, id0, id1, k > 0, k + 1 < kn ? 4 : last);
             mma_commit(&empty[ring.st]);
             if (k + 1 == kn) mma_commit(acc_full);
