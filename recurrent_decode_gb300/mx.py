@@ -227,6 +227,7 @@ class StateCache:
         if not self.data.is_cuda:
             raise TypeError("a state cache lies on a CUDA device")
         self.err = torch.zeros(1, dtype=torch.int32, device=self.data.device)
+        torch.cuda.current_stream(self.data.device).synchronize()  # a ctx may use it on a stream of its own
 
     def _states(self, fn, states, slots, entries):
         wkv, att, ffn = states

@@ -136,6 +136,7 @@ class PackedPrefixStateCache(PrefixStateCache):
         from .mx import StateCache
         self.states = StateCache(ctx.dims.n_layer, ctx.dims.n_head, n_entries, format)
         self._index = torch.arange(max(n_entries, ctx.n_slots), dtype=torch.int32, device=self.states.data.device)
+        torch.cuda.current_stream(self._index.device).synchronize()  # the ctx reads it on its own stream
 
     def _put(self, src_slot: int, entry: int) -> None:
         self.ctx.slots_save(self.states, self._index[src_slot:src_slot + 1], self._index[entry:entry + 1])

@@ -278,6 +278,75 @@ def test_product_on_its_own_stream_and_in_a_graph():
     assert torch.equal(out, fresh)
 
 
+def test_products_of_two_threads():
+    """Two host threads on one stream and on streams of their own: each keeps its own
+    rows on the way through the product."""
+    import threading
+    w = rd.mx4_quantize(torch.randn(300, 900, generator=cpu(12)).cuda())
+    xs = [torch.randn(40, 900, generator=cpu(20 + i)).cuda() for i in range(2)]
+    want = [rd.mx4_linear(x, w) for x in xs]
+    torch.cuda.synchronize()
+    for streams in ([torch.cuda.current_stream()] * 2, [torch.cuda.Stream(), torch.cuda.Stream()]):
+        wrong = []
+
+        def work(i):
+            with torch.cuda.stream(streams[i]):
+                for _ in range(200):
+                    y = rd.mx4_linear(xs[i], w)
+                streams[i].synchronize()
+                if not torch.equal(y, want[i]):
+                    wrong.append(i)
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not wrong
+
+
+def test_a_wait_that_gave_up_is_reported_once():
+    """The word that the kernel sets when a wait runs out, set here by the host."""
+    from recurrent_decode_gb300 import mx
+    x = torch.ones(2, 64, device="cuda")
+    w = rd.mx4_quantize(x)
+    rd.mx4_linear(x, w)
+    mx._err_word(torch.cuda.current_device()).fill_(8)
+    with pytest.raises(rd.RWKV7Error) as e:
+        rd.mx4_check()
+    assert e.value.code == rd.ETIMEOUT
+    rd.mx4_check()
+
+
+def test_rows_and_states_on_a_stream_and_in_a_graph():
+    x = torch.randn(9, 500, generator=cpu(13)).cuda()
+    st = tuple(t.cuda() for t in pool(1, 3, 2, 14))
+    cache = rd.StateCache(1, 2, 1, "mxint8")
+    m, out = rd.mx4_empty(9, 500, x.device), torch.empty_like(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        rd.mx4_quantize(x, out=m).dequantize(out=out)
+        cache.save(st, ints(0), ints(0))
+        cache.load(st, ints(0), ints(1))
+    s.synchronize()
+    same(out, nearest(x.double().cpu().numpy(), "mxfp4"))
+    want = nearest(st[0][:, 0].double().cpu().numpy(), "mxint8")
+    same(st[0][:, 1], want)
+    a, b, c = ints(0), ints(1), ints(2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rd.mx4_quantize(x, out=m).dequantize(out=out)
+        cache.save(st, b, a)
+        cache.load(st, a, c)
+    x.mul_(-3)
+    st[0][:, 1].mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    cache.check()
+    same(out, nearest(x.double().cpu().numpy(), "mxfp4"))
+    same(st[0][:, 2], 2 * want)
+
+
 def test_binding_refusals():
     w = rd.mx4_quantize(torch.ones(8, 64, device="cuda"))
     x = torch.ones(2, 64, device="cuda")
@@ -490,6 +559,26 @@ def test_packed_prefix_cache(fmt):
     assert cache.restore(other, 2) == 8
     cache.store(other, 2)  # evicts the entry after 12 tokens
     assert cache.evictions == 1 and cache.restore(body, 1) == 8
+    ctx.synchronize()
+    ctx.close()
+
+
+def test_slots_of_a_context_on_its_own_stream():
+    dims = synth.Dims("tiny")
+    s = torch.cuda.Stream()
+    ctx = rd.Rwkv7(dims, 2, stream=s)
+    state = [torch.randn(*a.shape, generator=cpu(30 + i)).numpy() for i, a in enumerate(ctx.get_state(0))]
+    cache = rd.StateCache(dims.n_layer, dims.n_head, 1, "mxint8")
+    zero, one = ints(0), ints(1)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        ctx.set_state(0, *state)
+        ctx.slot_reset(1)
+        ctx.slots_save(cache, zero, zero)
+        ctx.slots_load(cache, zero, one)
+        got = ctx.get_state(1)
+        assert np.array_equal(got[0].astype(np.float64), nearest(state[0], "mxint8")) and np.array_equal(got[1], state[1])
+        state[0] *= 2
     ctx.synchronize()
     ctx.close()
 
