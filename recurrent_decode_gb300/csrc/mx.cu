@@ -248,10 +248,12 @@ __global__ void __launch_bounds__(MXS_THREADS) mx_state_kernel(const MxStatePara
                : mx_pair_ok(p.slots, p.n_slots, entry, p.n_entries, i, p.err, hl == 0)))
         return;
     const int64_t heads = (int64_t)p.L * p.H;
-    uint8_t *codes = p.cache + (int64_t)entry * p.entry_bytes + mx_codes(hl, FMT);
-    uint8_t *scales = p.cache + (int64_t)entry * p.entry_bytes + mx_codes(heads, FMT) + (int64_t)hl * (MX_HEAD / MX_BLOCK);
-    float *shift = (float *)(p.cache + (int64_t)entry * p.entry_bytes + mx_codes(heads, FMT) +
-                             heads * (MX_HEAD / MX_BLOCK)) + (int64_t)layer * 2 * p.H * HS;
+    uint8_t *at = p.cache + (int64_t)entry * p.entry_bytes;
+    uint8_t *codes = at + mx_codes(hl, FMT);
+    at += mx_codes(heads, FMT);
+    uint8_t *scales = at + (int64_t)hl * (MX_HEAD / MX_BLOCK);
+    at += heads * (MX_HEAD / MX_BLOCK);
+    float *shift = (float *)at + (int64_t)layer * 2 * p.H * HS;
     float *st = p.wkv + (((int64_t)layer * p.n_slots + slot) * p.H + head) * MX_HEAD;
     if (threadIdx.x < 2 * HS / 4) {  // the head's 64 channels of both shift states
         const int which = threadIdx.x / (HS / 4), c = head * HS + (threadIdx.x % (HS / 4)) * 4;
@@ -359,7 +361,8 @@ int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, i
     p.ld = ld;
     p.mx = static_cast<uint8_t *>(const_cast<void *>(mx));
     p.kt = (int)((cols + MX_TILE_K - 1) / MX_TILE_K);
-    if (rows > (INT32_MAX - 4096) / p.kt) return mx_fail(err_msg, RWKV7_EINVAL, "%lld rows of %lld columns are too many", rows, cols);
+    if (rows > (INT32_MAX - 4096) / p.kt)
+        return mx_fail(err_msg, RWKV7_EINVAL, "%lld rows of %lld columns are too many", rows, cols);
     p.lines = (int)(rows * p.kt);
     const int step = 8 * size;  // bytes of a lane's eight values
     p.vec = (uintptr_t)x % step == 0 && (rows <= 1 || ld * size % step == 0);
@@ -393,20 +396,24 @@ int mx_states(bool save, MxStateParams &p, int32_t n, int32_t format, void *stre
         return mx_fail(err_msg, RWKV7_EINVAL, "layers, heads, slots and entries must be >= 1");
     if (n < 0 || n > RWKV7_STATES_MAX_PAIRS)
         return mx_fail(err_msg, RWKV7_EINVAL, "n=%lld is outside 0 .. %lld pairs a call", n, RWKV7_STATES_MAX_PAIRS);
-    if (format != RWKV7_MXFP4 && format != RWKV7_MXINT8) return mx_fail(err_msg, RWKV7_EINVAL, "unknown format %lld", format);
+    if (format != RWKV7_MXFP4 && format != RWKV7_MXINT8)
+        return mx_fail(err_msg, RWKV7_EINVAL, "unknown format %lld", format);
     if (n == 0) return RWKV7_OK;
     if (!p.wkv || !p.att || !p.ffn || !p.slots || !p.entries || !p.cache || !p.err)
         return mx_fail(err_msg, RWKV7_EINVAL, "null pointer argument");
     if (((uintptr_t)p.wkv & 31u) || (((uintptr_t)p.att | (uintptr_t)p.ffn | (uintptr_t)p.cache) & 15u))
-        return mx_fail(err_msg, RWKV7_EINVAL, "wkv must be 32-byte aligned, the shift states and the cache 16-byte aligned");
+        return mx_fail(err_msg, RWKV7_EINVAL,
+                       "wkv must be 32-byte aligned, the shift states and the cache 16-byte aligned");
     p.entry_bytes = (int64_t)rwkv7_state_entry_bytes(p.L, p.H, format);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.L * p.H), (unsigned)n);
     cfg.blockDim = dim3(MXS_THREADS);
     cfg.stream = static_cast<cudaStream_t>(stream);
     const void *fn = format == RWKV7_MXINT8
-                         ? (save ? (const void *)mx_state_kernel<MXINT8, true> : (const void *)mx_state_kernel<MXINT8, false>)
-                         : (save ? (const void *)mx_state_kernel<MXFP4, true> : (const void *)mx_state_kernel<MXFP4, false>);
+                         ? (save ? (const void *)mx_state_kernel<MXINT8, true>
+                                 : (const void *)mx_state_kernel<MXINT8, false>)
+                         : (save ? (const void *)mx_state_kernel<MXFP4, true>
+                                 : (const void *)mx_state_kernel<MXFP4, false>);
     void *args[] = {&p};
     return mx_done(err_msg, save ? "saving states" : "loading states", cudaLaunchKernelExC(&cfg, fn, args));
 }
@@ -436,7 +443,8 @@ int rwkv7_mx4_quantize(const void *d_x, int32_t dtype, int64_t rows, int64_t col
     MxRowsParams p;
     int rc = mx_rows_check(p, d_x, dtype, rows, cols, ld, d_mx, err_msg);
     if (rc || rows == 0) return rc;
-    return mx_done(err_msg, "quantising", mx_launch_rows(mx_quantize_fn(dtype), p, static_cast<cudaStream_t>(cuda_stream)));
+    return mx_done(err_msg, "quantising",
+                   mx_launch_rows(mx_quantize_fn(dtype), p, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y, int32_t dtype, int64_t ld,
@@ -444,7 +452,8 @@ int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y
     MxRowsParams p;
     int rc = mx_rows_check(p, d_y, dtype, rows, cols, ld, d_mx, err_msg);
     if (rc || rows == 0) return rc;
-    return mx_done(err_msg, "reading back", mx_launch_rows(mx_dequantize_fn(dtype), p, static_cast<cudaStream_t>(cuda_stream)));
+    return mx_done(err_msg, "reading back",
+                   mx_launch_rows(mx_dequantize_fn(dtype), p, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx, int64_t B, const void *d_w_mx, int64_t N,
@@ -453,11 +462,13 @@ int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx
     if (err_msg) *err_msg = "";
     if (!mx_size_ok(B, K) || !mx_size_ok(N, K) || N < 1)
         return mx_fail(err_msg, RWKV7_EINVAL, "B must be >= 0, N and K >= 1, all at most 2^24 (N=%lld, K=%lld)", N, K);
-    if (y_dtype < RWKV7_F32 || y_dtype > RWKV7_BF16) return mx_fail(err_msg, RWKV7_EINVAL, "unknown output dtype %lld", y_dtype);
+    if (y_dtype < RWKV7_F32 || y_dtype > RWKV7_BF16)
+        return mx_fail(err_msg, RWKV7_EINVAL, "unknown output dtype %lld", y_dtype);
     if (activation != RWKV7_ACT_NONE && activation != RWKV7_ACT_RELU2)
         return mx_fail(err_msg, RWKV7_EINVAL, "unknown activation %lld", activation);
     if (B > 1 && ldy < N) return mx_fail(err_msg, RWKV7_EINVAL, "output row stride %lld is below N=%lld", ldy, N);
-    if (B > ((int64_t)1 << 42) / N) return mx_fail(err_msg, RWKV7_EINVAL, "an output of %lld x %lld is too large", B, N);
+    if (B > ((int64_t)1 << 42) / N)
+        return mx_fail(err_msg, RWKV7_EINVAL, "an output of %lld x %lld is too large", B, N);
     if (B == 0) return RWKV7_OK;
     if (!d_x_mx || !d_w_mx || !d_y || !d_err) return mx_fail(err_msg, RWKV7_EINVAL, "null pointer argument");
     if ((uintptr_t)d_y % (y_dtype == RWKV7_F32 ? 4 : 2))
@@ -509,7 +520,8 @@ int rwkv7_states_save(const float *d_wkv, const float *d_shift_att, const float 
                       const char **err_msg) {
     MxStateParams p;
     memset(&p, 0, sizeof p);
-    p.wkv = const_cast<float *>(d_wkv), p.att = const_cast<float *>(d_shift_att), p.ffn = const_cast<float *>(d_shift_ffn);
+    p.wkv = const_cast<float *>(d_wkv);
+    p.att = const_cast<float *>(d_shift_att), p.ffn = const_cast<float *>(d_shift_ffn);
     p.L = n_layer, p.H = n_head, p.n_slots = n_slots, p.n_entries = n_entries;
     p.slots = d_slots, p.entries = d_entries;
     p.cache = static_cast<uint8_t *>(d_cache), p.err = d_err;

@@ -58,8 +58,8 @@ struct MxLinearParams {
 // type: MxType of y.  Where p.rows is given and the product is not one that quantises
 // them itself, quantize(ctx) is called first to launch the kernel that writes p.x; the
 // product then starts early, beside it.
-void launch_mx_linear(const MxLinearParams &p, int type, cudaStream_t stream, cudaError_t (*quantize)(void *), void *ctx,
-                      cudaError_t *e);
+void launch_mx_linear(const MxLinearParams &p, int type, cudaStream_t stream, cudaError_t (*quantize)(void *),
+                      void *ctx, cudaError_t *e);
 
 // The slot pool of a ctx, for saving and loading states (mx_ctx_states).
 struct MxCtxStates {

@@ -95,7 +95,8 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t adesc, uint64_t bd
 // Instruction descriptor: both sides 4-bit (code 1), powers of two as scales
 // (bit 23), K = 64; `half` selects the bytes 0-1 or 2-3 of every scale word.
 __device__ __forceinline__ uint32_t idesc_mxf4(int N, int half) {
-    return 1u << 7 | 1u << 10 | (uint32_t)(N >> 3) << 17 | 1u << 23 | 1u << 27 | (uint32_t)half << 5 | (uint32_t)half << 30;
+    return 1u << 7 | 1u << 10 | (uint32_t)(N >> 3) << 17 | 1u << 23 | 1u << 27 | (uint32_t)half << 5 |
+           (uint32_t)half << 30;
 }
 
 // 32 lanes x 16 columns on their way to v, which holds them after tmem_wait.
@@ -260,7 +261,8 @@ __device__ __forceinline__ void quantize_x(const MxLinearParams &p, uint8_t *xre
         const int k = line / p.B, r = line - k * p.B, blk = lane >> 2;
         uint8_t *rec = xres + k * MXL_XREC;
         uint32_t powers;
-        *(uint32_t *)(rec + MX_SCALE_BYTES + r * 128 + ((blk ^ (r & 7)) << 4) + (lane & 3) * 4) = mx4_line<T>(u[i], powers);
+        uint8_t *code = rec + MX_SCALE_BYTES + r * 128 + ((blk ^ (r & 7)) << 4) + (lane & 3) * 4;
+        *(uint32_t *)code = mx4_line<T>(u[i], powers);
         if ((lane & 15) == 0) *(uint32_t *)(rec + (blk >> 2) * 512 + r * 16) = powers;
     }
 }
@@ -591,8 +593,8 @@ void choose(MxLinearArgs &a, const MxClusters &most) {
 
 }  // namespace
 
-void launch_mx_linear(const MxLinearParams &p, int type, cudaStream_t stream, cudaError_t (*quantize)(void *), void *ctx,
-                      cudaError_t *e) {
+void launch_mx_linear(const MxLinearParams &p, int type, cudaStream_t stream, cudaError_t (*quantize)(void *),
+                      void *ctx, cudaError_t *e) {
     const void *fn = type == MX_F32   ? (const void *)mx_linear_kernel<float>
                      : type == MX_F16 ? (const void *)mx_linear_kernel<__half>
                                       : (const void *)mx_linear_kernel<__nv_bfloat16>;

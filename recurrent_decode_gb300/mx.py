@@ -181,8 +181,8 @@ def mx4_linear(x, w: MX4Matrix, out=None, out_dtype=None, activation=None):
         rows, cols, ldy, out_code = _rows(out, "out")
         if rows != B or cols != N or out.get_device() != dev:
             raise ValueError(f"out must be [{B}, {N}] on cuda:{dev}")
-    _call(load_library().rwkv7_mx4_linear, dev, src, code, ldx, data.data_ptr(), B, w.data.data_ptr(), N, K, out.data_ptr(), out_code,
-          ldy, act, _err_word(dev).data_ptr())
+    _call(load_library().rwkv7_mx4_linear, dev, src, code, ldx, data.data_ptr(), B, w.data.data_ptr(), N, K,
+          out.data_ptr(), out_code, ldy, act, _err_word(dev).data_ptr())
     return out
 
 
@@ -239,7 +239,8 @@ class StateCache:
             raise ValueError("states are wkv [L, slots, H, 64, 64] and two token shifts [L, slots, 64 H]")
         n_slots = wkv.shape[1]
         if wkv.shape != (L, n_slots, H, 64, 64) or att.shape != (L, n_slots, 64 * H) or ffn.shape != att.shape:
-            raise ValueError(f"states must be wkv [{L}, slots, {H}, 64, 64] and two token shifts [{L}, slots, {64 * H}]")
+            raise ValueError(f"states must be wkv [{L}, slots, {H}, 64, 64] and two token shifts "
+                             f"[{L}, slots, {64 * H}]")
         n = _pair_count(slots, entries, dev)
         _call(fn, dev.index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
               entries.data_ptr(), n, self.data.data_ptr(), self.n_entries, self.format, self.err.data_ptr())
