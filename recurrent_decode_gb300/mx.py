@@ -197,13 +197,15 @@ def mx4_check(device=None):
         raise RWKV7Error(ETIMEOUT, f"a bounded wait inside an MXFP4 product gave up (flags 0x{flags:x})")
 
 
-def _pair_count(slots, entries, dev):
+def _pair_count(slots, entries, dev: torch.device):
     for what, t in (("slots", slots), ("entries", entries)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous() \
+                or t.get_device() != dev.index:
             raise TypeError(f"{what} must be a contiguous int32 tensor on {dev}")
-    if slots.numel() != entries.numel():
+    n = slots.numel()
+    if n != entries.numel():
         raise ValueError("slots and entries differ in length")
-    return slots.numel()
+    return n
 
 
 class StateCache:
@@ -231,18 +233,19 @@ class StateCache:
 
     def _states(self, fn, states, slots, entries):
         wkv, att, ffn = states
-        dev, L, H = self.data.device, self.n_layer, self.n_head
+        dev, index, L, H = self.data.device, self.data.get_device(), self.n_layer, self.n_head
         for what, t in (("wkv", wkv), ("shift_att", att), ("shift_ffn", ffn)):
-            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_contiguous() or t.device != dev:
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or not t.is_contiguous() \
+                    or t.get_device() != index:
                 raise TypeError(f"{what} must be a contiguous float32 tensor on {dev}")
-        if wkv.dim() != 5 or att.dim() != 3:
-            raise ValueError("states are wkv [L, slots, H, 64, 64] and two token shifts [L, slots, 64 H]")
-        n_slots = wkv.shape[1]
-        if wkv.shape != (L, n_slots, H, 64, 64) or att.shape != (L, n_slots, 64 * H) or ffn.shape != att.shape:
+        shape = wkv.shape
+        n_slots = shape[1] if len(shape) == 5 else -1
+        shift = (L, n_slots, 64 * H)
+        if shape != (L, n_slots, H, 64, 64) or att.shape != shift or ffn.shape != shift:
             raise ValueError(f"states must be wkv [{L}, slots, {H}, 64, 64] and two token shifts "
                              f"[{L}, slots, {64 * H}]")
         n = _pair_count(slots, entries, dev)
-        _call(fn, dev.index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
+        _call(fn, index, wkv.data_ptr(), att.data_ptr(), ffn.data_ptr(), L, H, n_slots, slots.data_ptr(),
               entries.data_ptr(), n, self.data.data_ptr(), self.n_entries, self.format, self.err.data_ptr())
 
     def save(self, states, slots, entries):
