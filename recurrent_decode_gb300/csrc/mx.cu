@@ -8,10 +8,13 @@
 //            TB/s; one 7.2B state loaded into 48 slots, 1.7 GB: 259 us, 6.6 TB/s.
 //            Memory bounds them.  Stored 16 bytes a lane instead of 32 (two halves of
 //            each sector at different times) the load took 341 us.
-//   rows     4096 x 16384 bf16 to MXFP4, 170 MB: 28 us, 6.1 TB/s; back, 26.5 us, 6.4
-//            TB/s.  Addresses worked out line by line took 34 us (issue slots 74 %
-//            busy), one line a warp instead of four 59 and 45 us; for 64 x 2560 four
-//            lines a warp took 2.3 us instead of 1.6.
+//   rows     4096 x 16384 bf16 to MXFP4, 170 MB: 29.7 us, 5.7 TB/s; back, 27.2 us, 6.3
+//            TB/s.  Instructions come close to bounding them (issue slots 74-80 % busy):
+//            one line a warp instead of four took 59 and 45 us; for 64 x 2560 four lines
+//            a warp took 2.3 us instead of 1.6.  Four lines along a row instead of down a
+//            column tile took 28.1 us there, but 30 instead of 23 for 65536 x 300 fp16,
+//            whose rows end inside them.  Rows off the 16-byte grid, 8192 x 4001 fp16:
+//            25 us and 18 back, against 17.5 and 15 for 4000 columns.
 #include <cstdio>
 #include <cstring>
 
@@ -24,9 +27,10 @@ struct MxRowsParams {
     void *x;  // [rows] at ld
     int64_t cols, ld;
     uint8_t *mx;
-    int lines, kt;  // lines (rows x column tiles), column tiles
-    int per;        // consecutive lines a warp takes
+    int rows, kt;   // rows, column tiles
     int vec;        // the lanes' eight values start on 16-byte (fp32: 32-byte) boundaries in every row
+    int per;        // rows of one column tile that a warp takes (1 or MXQ_LINES)
+    int groups;     // such groups: ceil(rows / per) * kt
 };
 
 constexpr int MXQ_THREADS = 256;
@@ -35,105 +39,79 @@ constexpr int MXQ_LINES = 4;  // lines of a warp at most, their loads issued tog
 // with fewer lines one a warp spreads them over more SMs.
 constexpr int MXQ_MANY = 152 * 64;
 
-// Where a line lies: its values, a lane's four bytes of codes, the word of a half
-// line's powers.  Walks on line by line.
+// A warp's lines (a line: 256 columns of a row): up to MXQ_LINES consecutive rows of one
+// column tile.
 template <typename E>
-struct MxLine {
-    E *x;
-    uint8_t *code, *power;
-    int r, t;
-    __device__ __forceinline__ MxLine(const MxRowsParams &p, int line, int lane) {
-        r = line / p.kt;
-        t = line - r * p.kt;
-        row(p, lane);
-    }
-    __device__ __forceinline__ void row(const MxRowsParams &p, int lane) {
-        const int rr = r % MX_TILE_M, blk = lane >> 2;
-        uint8_t *tile = p.mx + ((int64_t)(r / MX_TILE_M) * p.kt + t) * MX_TILE_BYTES;
+struct MxLines {
+    E *x;            // the first line's values; the next lines' p.ld apart
+    uint8_t *codes;  // its codes; the next lines' 128 bytes apart
+    uint8_t *power;  // the word of powers of the lane's half; the next lines' 16 bytes apart
+    int at, place;   // a lane's bytes within its block's codes; the block's place in the first line
+    int n, cols;     // lines, columns of them that the matrix has
+    __device__ __forceinline__ MxLines(const MxRowsParams &p, int group, int lane) {
+        const int g = group / p.kt, t = group - g * p.kt, r = g * p.per, rr = r % MX_TILE_M;
+        n = min(p.per, p.rows - r);
+        cols = (int)min((int64_t)MX_TILE_K, p.cols - (int64_t)t * MX_TILE_K);
         x = (E *)p.x + r * p.ld + (int64_t)t * MX_TILE_K;
-        code = tile + MX_SCALE_BYTES + rr * 128 + ((blk ^ (rr & 7)) << 4) + (lane & 3) * 4;
-        power = tile + (blk >> 2) * 512 + (rr & 31) * 16 + (rr >> 5) * 4;
+        uint8_t *tile = p.mx + ((int64_t)(r / MX_TILE_M) * p.kt + t) * MX_TILE_BYTES;
+        codes = tile + MX_SCALE_BYTES + rr * 128;
+        power = tile + (lane >> 4) * 512 + (rr & 31) * 16 + (rr >> 5) * 4;
+        at = (lane & 3) * 4;
+        place = (lane >> 2) ^ (rr & 7);
     }
-    __device__ __forceinline__ void next(const MxRowsParams &p, int lane) {
-        if (++t < p.kt) {
-            x += MX_TILE_K;
-            code += MX_TILE_BYTES;
-            power += MX_TILE_BYTES;
-        } else {
-            t = 0;
-            ++r;
-            row(p, lane);
-        }
-    }
-    // whether `n` lines from here on are whole ones of one row on the 16-byte grid
-    __device__ __forceinline__ bool plain(const MxRowsParams &p, int n) const {
-        return n == MXQ_LINES && p.vec && (int64_t)(t + MXQ_LINES) * MX_TILE_K <= p.cols;
-    }
-    // how many of the line's 256 columns the matrix has
-    __device__ __forceinline__ int cols(const MxRowsParams &p) const {
-        return (int)min((int64_t)MX_TILE_K, p.cols - (int64_t)t * MX_TILE_K);
+    // Line l's.  Several lines start at a multiple of MXQ_LINES, so that l only sets low
+    // bits of the row.
+    __device__ __forceinline__ uint32_t *code(int l) const {
+        return (uint32_t *)(codes + l * 128 + ((place ^ l) << 4) + at);
     }
 };
 
-// A warp takes p.per consecutive lines (a line: 256 columns of a row), eight values a
-// lane.  Rows off the 16-byte grid are read value by value, neighbours by
-// neighbouring lanes, and turned through shared memory.
+// Eight values a lane.  Rows off the 16-byte grid are turned through shared memory.
 template <int T>
 __global__ void __launch_bounds__(MXQ_THREADS) mx4_quantize_kernel(const MxRowsParams p) {
     using L = MxElem<T>;
     using E = typename L::type;
-    __shared__ __align__(16) E turn[MXQ_THREADS / 32][MX_TILE_K];
+    __shared__ __align__(16) E room[MXQ_THREADS / 32][MX_TILE_K];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = (blockIdx.x * (MXQ_THREADS / 32) + warp) * p.per;
+    const int group = blockIdx.x * (MXQ_THREADS / 32) + warp;
     pdl_launch();  // a product of these rows may start fetching its weights
-    const int n = min(p.per, p.lines - first);
-    if (n <= 0) return;
+    if (group >= p.groups) return;
+    const MxLines<E> in(p, group, lane);
     typename L::Eight u[MXQ_LINES];
-    MxLine<E> at(p, first, lane);
-    if (at.plain(p, n)) {  // the usual case, at fixed distances
+    uint32_t w;
+    if (p.vec && in.n == MXQ_LINES && in.cols == MX_TILE_K) {  // the usual case
 #pragma unroll
-        for (int l = 0; l < MXQ_LINES; ++l) L::load(u[l], at.x + l * MX_TILE_K + lane * 8);
+        for (int l = 0; l < MXQ_LINES; ++l) L::load(u[l], in.x + l * p.ld + lane * 8);
 #pragma unroll
         for (int l = 0; l < MXQ_LINES; ++l) {
-            uint32_t w;
-            *(uint32_t *)(at.code + l * MX_TILE_BYTES) = mx4_line<T>(u[l], w);
-            if ((lane & 15) == 0) *(uint32_t *)(at.power + l * MX_TILE_BYTES) = w;
+            *in.code(l) = mx4_line<T>(u[l], w);
+            if ((lane & 15) == 0) *(uint32_t *)(in.power + l * 16) = w;
         }
         return;
     }
-    const MxLine<E> start = at;
+    E edge[MXQ_LINES];
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
-        if (l >= n) break;
-        const int cols = at.cols(p);
-        if (p.vec && lane * 8 + 8 <= cols) {
-            L::load(u[l], at.x + lane * 8);
+        if (l >= in.n) break;
+        const E *x = in.x + l * p.ld;
+        if (!p.vec) {
+            L::gather(u[l], edge[l], x, in.cols, lane);
+        } else if (lane * 8 + 8 <= in.cols) {
+            L::load(u[l], x + lane * 8);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = p.vec ? lane * 8 + i : i * 32 + lane;
-                L::set(u[l], i, c < cols ? at.x[c] : L::down(0.0f));
-            }
+            for (int i = 0; i < 8; ++i) L::set(u[l], i, lane * 8 + i < in.cols ? x[lane * 8 + i] : L::down(0.0f));
         }
-        at.next(p, lane);
     }
-    at = start;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
-        if (l >= n) break;
+        if (l >= in.n) break;
         if (!p.vec) {
-            E *tw = turn[warp];
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tw[i * 32 + lane] = ((const E *)&u[l])[i];
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(u[l]) / 16; ++i) ((uint4 *)&u[l])[i] = ((const uint4 *)(tw + lane * 8))[i];
+            L::turn(u[l], edge[l], in.x + l * p.ld, room[warp], lane);
         }
-        uint32_t w;
-        *(uint32_t *)at.code = mx4_line<T>(u[l], w);
-        if ((lane & 15) == 0) *(uint32_t *)at.power = w;
-        at.next(p, lane);
+        *in.code(l) = mx4_line<T>(u[l], w);
+        if ((lane & 15) == 0) *(uint32_t *)(in.power + l * 16) = w;
     }
 }
 
@@ -141,59 +119,46 @@ template <int T>
 __global__ void __launch_bounds__(MXQ_THREADS) mx4_dequantize_kernel(const MxRowsParams p) {
     using L = MxElem<T>;
     using E = typename L::type;
-    __shared__ __align__(16) float turn[MXQ_THREADS / 32][MX_TILE_K];
+    __shared__ __align__(16) E room[MXQ_THREADS / 32][MX_TILE_K];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = (blockIdx.x * (MXQ_THREADS / 32) + warp) * p.per;
-    const int n = min(p.per, p.lines - first);
-    if (n <= 0) return;
+    const int group = blockIdx.x * (MXQ_THREADS / 32) + warp;
+    if (group >= p.groups) return;
+    const MxLines<E> out(p, group, lane);
     uint32_t code[MXQ_LINES], s[MXQ_LINES];
-    MxLine<E> at(p, first, lane);
-    if (at.plain(p, n)) {  // the usual case, at fixed distances
+    if (p.vec && out.n == MXQ_LINES && out.cols == MX_TILE_K) {  // the usual case
 #pragma unroll
-        for (int l = 0; l < MXQ_LINES; ++l) {
-            code[l] = *(const uint32_t *)(at.code + l * MX_TILE_BYTES);
-            s[l] = at.power[l * MX_TILE_BYTES + ((lane >> 2) & 3)];
-        }
+        for (int l = 0; l < MXQ_LINES; ++l) code[l] = *out.code(l), s[l] = out.power[l * 16 + ((lane >> 2) & 3)];
 #pragma unroll
         for (int l = 0; l < MXQ_LINES; ++l) {
             float v[8];
             mx4_values(code[l], s[l], v);
-            L::store(at.x + l * MX_TILE_K + lane * 8, v);
+            L::store(out.x + l * p.ld + lane * 8, v);
         }
         return;
     }
-    const MxLine<E> start = at;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
-        if (l >= n) break;
-        code[l] = *(const uint32_t *)at.code;
-        s[l] = at.power[(lane >> 2) & 3];
-        at.next(p, lane);
+        if (l >= out.n) break;
+        code[l] = *out.code(l), s[l] = out.power[l * 16 + ((lane >> 2) & 3)];
     }
-    at = start;
 #pragma unroll
     for (int l = 0; l < MXQ_LINES; ++l) {
-        if (l >= n) break;
+        if (l >= out.n) break;
         float v[8];
         mx4_values(code[l], s[l], v);
-        const int cols = at.cols(p);
-        if (p.vec && lane * 8 + 8 <= cols) {
-            L::store(at.x + lane * 8, v);
-        } else if (p.vec) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (lane * 8 + i < cols) at.x[lane * 8 + i] = L::down(v[i]);
+        E *x = out.x + l * p.ld;
+        if (!p.vec) {
+            __syncwarp();
+            L::store_aligned(room[warp] + lane * 8, v);
+            __syncwarp();
+            L::scatter(x, room[warp], out.cols, lane);
+        } else if (lane * 8 + 8 <= out.cols) {
+            L::store(x + lane * 8, v);
         } else {
-            float *tw = turn[warp];
-            __syncwarp();
-            *(float4 *)&tw[lane * 8] = *(const float4 *)&v[0];
-            *(float4 *)&tw[lane * 8 + 4] = *(const float4 *)&v[4];
-            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (i * 32 + lane < cols) at.x[i * 32 + lane] = L::down(tw[i * 32 + lane]);
+                if (lane * 8 + i < out.cols) x[lane * 8 + i] = L::down(v[i]);
         }
-        at.next(p, lane);
     }
 }
 
@@ -363,17 +328,17 @@ int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, i
     p.kt = (int)((cols + MX_TILE_K - 1) / MX_TILE_K);
     if (rows > (INT32_MAX - 4096) / p.kt)
         return mx_fail(err_msg, RWKV7_EINVAL, "%lld rows of %lld columns are too many", rows, cols);
-    p.lines = (int)(rows * p.kt);
+    p.rows = (int)rows;
     const int step = 8 * size;  // bytes of a lane's eight values
     p.vec = (uintptr_t)x % step == 0 && (rows <= 1 || ld * size % step == 0);
+    p.per = rows * p.kt >= MXQ_MANY ? MXQ_LINES : 1;
+    p.groups = (int)((rows + p.per - 1) / p.per * p.kt);
     return RWKV7_OK;
 }
 
 cudaError_t mx_launch_rows(const void *kernel, MxRowsParams &p, cudaStream_t stream) {
-    p.per = p.lines >= MXQ_MANY ? MXQ_LINES : 1;
-    const int per = MXQ_THREADS / 32 * p.per;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.lines + (int64_t)per - 1) / per));
+    cfg.gridDim = dim3((unsigned)((p.groups + MXQ_THREADS / 32 - 1) / (MXQ_THREADS / 32)));
     cfg.blockDim = dim3(MXQ_THREADS);
     cfg.stream = stream;
     void *args[] = {&p};

@@ -163,8 +163,30 @@ struct MxElem<MX_F32> {
     };
     static __device__ __forceinline__ void load(Eight &u, const float *p) { ld_v8(u.v, p); }
     static __device__ __forceinline__ void store(float *p, const float (&v)[8]) { st_v8(p, v); }
+    static __device__ __forceinline__ void store_aligned(float *p, const float (&v)[8]) {  // to shared memory
+        *(float4 *)p = *(const float4 *)&v[0];
+        *(float4 *)(p + 4) = *(const float4 *)&v[4];
+    }
     static __device__ __forceinline__ void set(Eight &u, int i, float v) { u.v[i] = v; }
     static __device__ __forceinline__ uint32_t top(const Eight &u) { return mx_quad_top(u.v); }
+    // A line of `cols` values off the grid, neighbours by neighbouring lanes, and its
+    // turn through shared memory (room for 256) to eight neighbours a lane; the same back.
+    static __device__ __forceinline__ void gather(Eight &u, float &, const float *p, int cols, int lane) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u.v[i] = i * 32 + lane < cols ? p[i * 32 + lane] : 0.0f;
+    }
+    static __device__ __forceinline__ void turn(Eight &u, float, const float *, float *room, int lane) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) room[i * 32 + lane] = u.v[i];
+        __syncwarp();
+        *(float4 *)&u.v[0] = *(const float4 *)(room + lane * 8);
+        *(float4 *)&u.v[4] = *(const float4 *)(room + lane * 8 + 4);
+    }
+    static __device__ __forceinline__ void scatter(float *p, const float *room, int cols, int lane) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i * 32 + lane < cols) p[i * 32 + lane] = room[i * 32 + lane];
+    }
     static __device__ __forceinline__ float up(const Eight &u, int i) { return u.v[i]; }
     static __device__ __forceinline__ float down(float v) { return v; }
 };
@@ -178,6 +200,49 @@ struct MxHalves {
     };
     static __device__ __forceinline__ void load(Eight &u, const E *p) { *(uint4 *)u.w = *(const uint4 *)p; }
     static __device__ __forceinline__ void set(Eight &u, int i, E v) { ((E *)u.w)[i] = v; }
+    // As for fp32, by words of two values from the first word on that lies in the row;
+    // the value before it, where there is one, is `edge` (lane 0).
+    static __device__ __forceinline__ int skip(const E *p) { return (int)((uintptr_t)p >> 1 & 1u); }
+    static __device__ __forceinline__ void gather(Eight &u, E &edge, const E *p, int cols, int lane) {
+        const int e0 = skip(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = e0 + (j * 32 + lane) * 2;
+            u.w[j] = e + 2 <= cols ? *(const uint32_t *)(p + e) : (e < cols ? *(const unsigned short *)(p + e) : 0u);
+        }
+        if (e0 && lane == 0) edge = p[0];
+    }
+    static __device__ __forceinline__ void turn(Eight &u, E edge, const E *p, E *room, int lane) {
+        const int e0 = skip(p);
+        unsigned short *h = (unsigned short *)room;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = e0 + (j * 32 + lane) * 2;
+            if (e0 == 0) {
+                ((uint32_t *)room)[j * 32 + lane] = u.w[j];
+            } else {
+                h[e] = (unsigned short)u.w[j];
+                if (e < 255) h[e + 1] = (unsigned short)(u.w[j] >> 16);
+            }
+        }
+        if (e0 && lane == 0) room[0] = edge;
+        __syncwarp();
+        *(uint4 *)u.w = *(const uint4 *)(room + lane * 8);
+    }
+    static __device__ __forceinline__ void scatter(E *p, const E *room, int cols, int lane) {
+        const int e0 = skip(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = e0 + (j * 32 + lane) * 2;
+            if (e + 2 <= cols) {
+                const unsigned short *h = (const unsigned short *)room + e;
+                *(uint32_t *)(p + e) = (uint32_t)h[0] | (uint32_t)h[1] << 16;
+            } else if (e < cols) {
+                p[e] = room[e];
+            }
+        }
+        if (e0 && lane == 0) p[0] = room[0];
+    }
     static __device__ __forceinline__ uint32_t top_bits(const Eight &u) {
         uint32_t m = __vmaxu2(__vmaxu2(u.w[0] & 0x7FFF7FFFu, u.w[1] & 0x7FFF7FFFu),
                               __vmaxu2(u.w[2] & 0x7FFF7FFFu, u.w[3] & 0x7FFF7FFFu));
@@ -195,6 +260,7 @@ struct MxElem<MX_F16> : MxHalves<__half> {
         return __half2float(((const __half *)u.w)[i]);
     }
     static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ void store_aligned(__half *p, const float (&v)[8]) { store(p, v); }
     static __device__ __forceinline__ void store(__half *p, const float (&v)[8]) {
         __half2 h[4];
 #pragma unroll
@@ -209,6 +275,7 @@ struct MxElem<MX_BF16> : MxHalves<__nv_bfloat16> {
         return __uint_as_float(i & 1 ? u.w[i >> 1] & 0xFFFF0000u : u.w[i >> 1] << 16);
     }
     static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ void store_aligned(__nv_bfloat16 *p, const float (&v)[8]) { store(p, v); }
     static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
         __nv_bfloat162 h[4];
 #pragma unroll
