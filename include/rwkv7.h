@@ -400,10 +400,10 @@ RWKV7_API size_t rwkv7_state_entry_bytes(int32_t n_layer, int32_t n_head, int32_
  * [n_layer][n_slots][n_head][64][64], d_shift_att and d_shift_ffn
  * [n_layer][n_slots][64 * n_head], 16-byte aligned (d_wkv 32).  The wkv states are quantised
  * along their rows (the key channels), the shift states kept exactly.  Several
- * pairs may read the same slot or entry.  Where two pairs write the same one the
- * first is carried out, the others are not, and bit 4 is set in *d_err (a device
- * word the caller zeroed); an index out of range sets bit 1 and its pair is left
- * out. */
+ * pairs may read the same slot or entry.  An index out of range sets bit 1 in
+ * *d_err (a device word the caller zeroed) and its pair is left out.  Where two of
+ * the other pairs write the same slot or entry the first is carried out, the others
+ * are not, and bit 4 is set. */
 RWKV7_API int rwkv7_states_save(const float *d_wkv, const float *d_shift_att, const float *d_shift_ffn,
                                 int32_t n_layer, int32_t n_head, int32_t n_slots, const int32_t *d_slots,
                                 const int32_t *d_entries, int32_t n, void *d_cache, int32_t n_entries, int32_t format,
