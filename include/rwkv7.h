@@ -396,14 +396,15 @@ RWKV7_API size_t rwkv7_state_entry_bytes(int32_t n_layer, int32_t n_head, int32_
 /* Save the states of n slots into entries of d_cache (n_entries times
  * rwkv7_state_entry_bytes bytes, 16-byte aligned), or load entries into slots:
  * pair i is slot d_slots[i] and entry d_entries[i] (device int32 [n],
- * 0 <= n <= RWKV7_STATES_MAX_PAIRS).  The pool is fp32, as the ctx keeps it: d_wkv
- * [n_layer][n_slots][n_head][64][64], d_shift_att and d_shift_ffn
- * [n_layer][n_slots][64 * n_head], 16-byte aligned (d_wkv 32).  The wkv states are quantised
- * along their rows (the key channels), the shift states kept exactly.  Several
- * pairs may read the same slot or entry.  An index out of range sets bit 1 in
- * *d_err (a device word the caller zeroed) and its pair is left out.  Where two of
- * the other pairs write the same slot or entry the first is carried out, the others
- * are not, and bit 4 is set. */
+ * 0 <= n <= RWKV7_STATES_MAX_PAIRS).  What an entry holds before its first save is
+ * the caller's: zeros load as the state of a slot after a reset.  The pool is fp32,
+ * as the ctx keeps it: d_wkv [n_layer][n_slots][n_head][64][64], d_shift_att and
+ * d_shift_ffn [n_layer][n_slots][64 * n_head], 16-byte aligned (d_wkv 32).  The wkv
+ * states are quantised along their rows (the key channels), the shift states kept
+ * exactly.  Several pairs may read the same slot or entry.  An index out of range
+ * sets bit 1 in *d_err (a device word the caller zeroed) and its pair is left out.
+ * Where two of the other pairs write the same slot or entry the first is carried
+ * out, the others are not, and bit 4 is set. */
 RWKV7_API int rwkv7_states_save(const float *d_wkv, const float *d_shift_att, const float *d_shift_ffn,
                                 int32_t n_layer, int32_t n_head, int32_t n_slots, const int32_t *d_slots,
                                 const int32_t *d_entries, int32_t n, void *d_cache, int32_t n_entries, int32_t format,

@@ -214,7 +214,8 @@ class StateCache:
     slots_load move a ctx's slots; save and load a pool the caller owns.
 
     MXINT8 keeps every value to within 1/127 of the largest of its block of 32 along
-    a state row, MXFP4 to within 1/5; token-shift states are kept exactly."""
+    a state row, MXFP4 to within 1/5; token-shift states are kept exactly.  An entry
+    that nothing was saved to holds the state of a slot after a reset."""
 
     def __init__(self, n_layer: int, n_head: int, n_entries: int, format: str = "mxint8", device=None):
         if format not in _FORMATS:
@@ -224,7 +225,7 @@ class StateCache:
         self.entry_bytes = load_library().rwkv7_state_entry_bytes(self.n_layer, self.n_head, self.format)
         if self.entry_bytes == 0 or self.n_entries < 1:
             raise RWKV7Error(EINVAL, "layers, heads and entries must be >= 1")
-        self.data = torch.empty(self.n_entries * self.entry_bytes, dtype=torch.uint8,
+        self.data = torch.zeros(self.n_entries * self.entry_bytes, dtype=torch.uint8,
                                 device="cuda" if device is None else device)
         if not self.data.is_cuda:
             raise TypeError("a state cache lies on a CUDA device")

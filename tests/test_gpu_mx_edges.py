@@ -44,3 +44,16 @@ def test_of_good_bad_and_good_the_first_good_is_carried_out():
     with pytest.raises(rd.RWKV7Error, match="0x5"):
         cache.check()
     same(st[0][:, 3], nearest(host[0][:, 1].double().numpy(), "mxint8"))
+
+
+@pytest.mark.parametrize("fmt", ["mxint8", "mxfp4"])
+def test_an_entry_never_saved_is_a_fresh_state(fmt):
+    size = rd.StateCache(2, 2, 3, fmt).data.numel()
+    torch.full((size,), 0x5B, dtype=torch.uint8, device="cuda")  # what the allocator may hand out next
+    cache = rd.StateCache(2, 2, 3, fmt)
+    st = tuple(t.cuda() for t in pool(2, 3, 2, 33))
+    kept = tuple(t[:, 1].clone() for t in st)
+    cache.load(st, ints(0, 2), ints(2, 0))
+    cache.check()
+    for t, k in zip(st, kept):
+        assert bool((t[:, 0] == 0).all()) and bool((t[:, 2] == 0).all()) and torch.equal(t[:, 1], k)
