@@ -289,14 +289,16 @@ class Rwkv7:
 
     def slots_save(self, cache: "StateCache", slots, entries):
         """rwkv7_slots_save: keep the states of `slots` in `entries` of a StateCache
-        of this model's layers and heads (int32 CUDA tensors of equal length)."""
+        of this model's layers and heads (int32 CUDA tensors of equal length).  It runs
+        on the context's stream, after what the current stream has in flight; the
+        tensors may be dropped at once, but not overwritten before it is done."""
         n = self._pairs(cache, slots, entries)
         self._check(self.lib.rwkv7_slots_save(self.h, slots.data_ptr(), entries.data_ptr(), n, cache.data.data_ptr(),
                                               cache.n_entries, cache.format))
 
     def slots_load(self, cache: "StateCache", entries, slots):
         """rwkv7_slots_load: put the kept states of `entries` into `slots`, whose
-        occurrence counts and draw counters restart."""
+        occurrence counts and draw counters restart.  On streams as slots_save."""
         n = self._pairs(cache, slots, entries)
         self._check(self.lib.rwkv7_slots_load(self.h, slots.data_ptr(), entries.data_ptr(), n, cache.data.data_ptr(),
                                               cache.n_entries, cache.format))
@@ -304,8 +306,11 @@ class Rwkv7:
     def _pairs(self, cache, slots, entries):
         if (cache.n_layer, cache.n_head) != (self.dims.n_layer, self.dims.n_head):
             raise ValueError("the cache was made for another number of layers or heads")
-        from .mx import _pair_count
-        return _pair_count(slots, entries, cache.data.device)
+        from .mx import _follow, _pair_count
+        dev = cache.data.device
+        n = _pair_count(slots, entries, dev)
+        _follow(self.stream, cache.data, slots, entries)
+        return n
 
     def set_sampling(self, slot: int, temperature=1.0, top_p=0.3, top_k=0, presence=0.0,
                      frequency=1.0, penalty_decay=0.996, seed=0, greedy=False):

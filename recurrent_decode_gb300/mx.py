@@ -197,6 +197,16 @@ def mx4_check(device=None):
         raise RWKV7Error(ETIMEOUT, f"a bounded wait inside an MXFP4 product gave up (flags 0x{flags:x})")
 
 
+def _follow(stream, *tensors):
+    """For a kernel that `stream` runs on tensors of the current stream: it comes after
+    what that has in flight, and their memory is not handed out again before it ends."""
+    current = torch.cuda.current_stream(stream.device)
+    if current != stream:
+        stream.wait_stream(current)
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _pair_count(slots, entries, dev: torch.device):
     for what, t in (("slots", slots), ("entries", entries)):
         if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous() \

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import recurrent_decode_gb300 as rd
+import synth
 from _mx_reference import nearest
 from test_gpu_mx import cpu, ints, pool, same
 
@@ -57,3 +58,59 @@ def test_an_entry_never_saved_is_a_fresh_state(fmt):
     cache.check()
     for t, k in zip(st, kept):
         assert bool((t[:, 0] == 0).all()) and bool((t[:, 2] == 0).all()) and torch.equal(t[:, 1], k)
+
+
+# ------------------------------------------------------------------ streams
+@pytest.fixture
+def own_stream():
+    """A context of four slots on a stream of its own, each with its own state."""
+    dims = synth.Dims("tiny")
+    ctx = rd.Rwkv7(dims, 4, stream=torch.cuda.Stream())
+    states = [[torch.randn(*a.shape, generator=cpu(40 + s)).numpy() for a in ctx.get_state(0)] for s in range(4)]
+    for s in range(4):
+        ctx.set_state(s, *states[s])
+    torch.cuda.synchronize()
+    yield ctx, dims, states
+    ctx.synchronize()
+    ctx.close()
+
+
+def filled(v):
+    """An index that a kernel of the current stream writes (no copy, which would wait)."""
+    return torch.full((1,), v, dtype=torch.int32, device="cuda")
+
+
+SOME_MS = 100_000_000  # clock ticks: 50 ms
+
+
+def test_indices_of_a_busy_stream_are_read_after_they_are_written(own_stream):
+    ctx, dims, states = own_stream
+    cache = rd.StateCache(dims.n_layer, dims.n_head, 2)
+    torch.cuda._sleep(SOME_MS)
+    ctx.slots_save(cache, filled(2), filled(1))
+    torch.cuda._sleep(SOME_MS)
+    ctx.slots_load(cache, filled(1), filled(3))
+    ctx.synchronize()
+    got = ctx.get_state(3)
+    same(torch.from_numpy(got[0]), nearest(states[2][0], "mxint8"))
+    assert (got[1] == states[2][1]).all()
+
+
+def test_indices_and_cache_may_be_dropped_at_once(own_stream):
+    """Their memory is not handed out again while the context's stream has yet to read it."""
+    ctx, dims, states = own_stream
+    cache = rd.StateCache(dims.n_layer, dims.n_head, 2)
+    size = cache.data.numel()
+    with torch.cuda.stream(ctx.stream):
+        torch.cuda._sleep(SOME_MS)
+    ctx.slots_save(cache, filled(2), filled(1))
+    others = [filled(0) for _ in range(8)]  # valid ones, in the memory of those if it were free
+    ctx.slots_load(cache, filled(1), filled(3))
+    others += [filled(0) for _ in range(8)]
+    del cache
+    others.append(torch.full((size,), 0x33, dtype=torch.uint8, device="cuda"))
+    ctx.synchronize()
+    got = ctx.get_state(3)
+    same(torch.from_numpy(got[0]), nearest(states[2][0], "mxint8"))
+    assert (got[2] == states[2][2]).all()
+    assert (ctx.get_state(0)[0] == states[0][0]).all()

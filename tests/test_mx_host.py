@@ -1,0 +1,74 @@
+"""What the binding of the microscaled operators does on the host: the order of streams,
+the memory that calls keep, who makes the error word, indices of the packed prefix
+cache.  No GPU: the library, streams and tensors are stand-ins."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import recurrent_decode_gb300 as rd
+from recurrent_decode_gb300 import mx
+
+CUDA0, CUDA1 = torch.device("cuda", 0), torch.device("cuda", 1)
+
+
+# ------------------------------------------------------------------ streams
+class Stream:
+    def __init__(self, name, log, device=CUDA0):
+        self.name, self.log, self.device = name, log, device
+
+    def wait_stream(self, other):
+        self.log.append(f"{self.name} waits for {other.name}")
+
+
+class Tensor:
+    def __init__(self, name, log, device=CUDA0):
+        self.name, self.log, self.device = name, log, device
+
+    def data_ptr(self):
+        return 4096
+
+    def record_stream(self, stream):
+        self.log.append(f"{self.name} kept for {stream.name}")
+
+
+def context(stream, log):
+    ctx = rd.Rwkv7.__new__(rd.Rwkv7)
+    ctx.h, ctx.stream, ctx.dims = None, stream, SimpleNamespace(n_layer=2, n_head=3)
+    ctx.lib = SimpleNamespace(rwkv7_slots_save=lambda *a: log.append("save") or 0,
+                              rwkv7_slots_load=lambda *a: log.append("load") or 0)
+    return ctx
+
+
+class Log(list):
+    current = None  # stream
+
+
+@pytest.fixture
+def log(monkeypatch):
+    log = Log()
+    monkeypatch.setattr(mx, "_pair_count", lambda slots, entries, dev: 1)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: log.current)
+    return log
+
+
+def cache_of(log, device=CUDA0):
+    return SimpleNamespace(n_layer=2, n_head=3, n_entries=4, format=1, data=Tensor("cache", log, device))
+
+
+@pytest.mark.parametrize("what", ["save", "load"])
+def test_slots_on_a_stream_of_their_own_follow_the_current_one(log, what):
+    log.current = Stream("current", log)
+    ctx, cache = context(Stream("own", log), log), cache_of(log)
+    a, b = Tensor("a", log), Tensor("b", log)
+    (ctx.slots_save if what == "save" else ctx.slots_load)(cache, a, b)
+    assert log.index("own waits for current") < log.index(what)
+    for name in ("cache", "a", "b"):
+        assert f"{name} kept for own" in log
+
+
+def test_slots_on_the_current_stream_wait_for_nothing(log):
+    log.current = Stream("current", log)
+    ctx, cache = context(log.current, log), cache_of(log)
+    ctx.slots_save(cache, Tensor("a", log), Tensor("b", log))
+    assert log == ["save"]
