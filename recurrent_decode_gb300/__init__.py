@@ -308,6 +308,8 @@ class Rwkv7:
             raise ValueError("the cache was made for another number of layers or heads")
         from .mx import _follow, _pair_count
         dev = cache.data.device
+        if dev != self.stream.device:
+            raise ValueError(f"the cache is on {dev}, the context on {self.stream.device}")
         n = _pair_count(slots, entries, dev)
         _follow(self.stream, cache.data, slots, entries)
         return n

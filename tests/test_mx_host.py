@@ -72,3 +72,12 @@ def test_slots_on_the_current_stream_wait_for_nothing(log):
     ctx, cache = context(log.current, log), cache_of(log)
     ctx.slots_save(cache, Tensor("a", log), Tensor("b", log))
     assert log == ["save"]
+
+
+def test_slots_refuse_a_cache_of_another_device(log):
+    log.current = Stream("current", log)
+    ctx = context(Stream("own", log), log)
+    for call in (ctx.slots_save, ctx.slots_load):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call(cache_of(log, CUDA1), Tensor("a", log, CUDA1), Tensor("b", log, CUDA1))
+    assert log == []
