@@ -27,14 +27,18 @@ _current_device = torch._C._cuda_getDevice
 _ROOM = 2 << 20  # 128 rows of 30,000 columns
 _kept = threading.local()  # (device, stream) -> bytes of _room
 _err: dict[int, torch.Tensor] = {}  # per device: the word in which kernels latch errors
+_err_lock = threading.Lock()
 
 
 def _err_word(dev: int) -> torch.Tensor:
     w = _err.get(dev)
     if w is None:
-        w = torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
-        torch.cuda.current_stream(dev).synchronize()  # other streams will use it
-        _err[dev] = w
+        with _err_lock:  # of threads that come at once, the first makes it
+            w = _err.get(dev)
+            if w is None:
+                w = torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
+                torch.cuda.current_stream(dev).synchronize()  # other streams will use it
+                _err[dev] = w
     return w
 
 

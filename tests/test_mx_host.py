@@ -81,3 +81,27 @@ def test_slots_refuse_a_cache_of_another_device(log):
         with pytest.raises(ValueError, match="cuda:1"):
             call(cache_of(log, CUDA1), Tensor("a", log, CUDA1), Tensor("b", log, CUDA1))
     assert log == []
+
+
+# ------------------------------------------------------------------ the error word
+def test_threads_that_come_at_once_share_one_error_word(monkeypatch):
+    import threading
+    import time
+
+    def zeros(*a, **k):
+        time.sleep(0.02)  # long enough for all threads to find no word
+        return object()
+    monkeypatch.setattr(mx, "_err", {})
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: SimpleNamespace(synchronize=lambda: None))
+    start, words = threading.Barrier(8), []
+
+    def first_call():
+        start.wait()
+        words.append(mx._err_word(0))
+    threads = [threading.Thread(target=first_call) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(words) == 8 and all(w is mx._err[0] for w in words)
