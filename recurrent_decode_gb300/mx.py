@@ -55,12 +55,20 @@ def _call(fn, dev: int, *args):
         raise RWKV7Error(rc, (msg.value or b"").decode())
 
 
+def _capturing(dev: int) -> bool:
+    """Whether the current stream of device `dev` is being captured."""
+    if dev == _current_device():
+        return torch._C._cuda_isCurrentStreamCapturing()  # (which asks for the current device's)
+    with torch.cuda.device(dev):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def _room(n: int, dev: int) -> torch.Tensor:
     """n bytes for x quantised on the way.  Up to _ROOM of them are kept for the next
     call of the same host thread on the same stream, whose kernels run after this
     call's (an allocation between two launches costs 3 us, a small product takes 6);
     a graph gets bytes of its own."""
-    if n > _ROOM or torch._C._cuda_isCurrentStreamCapturing():
+    if n > _ROOM or _capturing(dev):
         return torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
     key = dev, _raw_stream(dev)
     rooms = _kept.__dict__

@@ -105,3 +105,48 @@ def test_threads_that_come_at_once_share_one_error_word(monkeypatch):
     for t in threads:
         t.join()
     assert len(words) == 8 and all(w is mx._err[0] for w in words)
+
+
+# ------------------------------------------------------------------ memory kept between calls
+class Devices:
+    """Two devices, each with a current stream, which may be one that is being captured."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.capturing, self.made = 0, set(), []
+        self.stream = {0: 0, 1: 0}
+        fakes = self
+
+        class device:
+            def __init__(self, dev):
+                self.dev = dev
+
+            def __enter__(self):
+                self.before, fakes.current = fakes.current, self.dev
+
+            def __exit__(self, *a):
+                fakes.current = self.before
+
+        def empty(n, dtype, device):
+            self.made.append(SimpleNamespace(n=n, device=device))
+            return self.made[-1]
+        monkeypatch.setattr(mx, "_kept", SimpleNamespace())
+        monkeypatch.setattr(mx, "_current_device", lambda: self.current)
+        monkeypatch.setattr(mx, "_raw_stream", lambda dev: self.stream[dev])
+        monkeypatch.setattr(torch.cuda, "device", device)
+        monkeypatch.setattr(torch, "empty", empty)
+        monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: self.current in self.capturing,
+                            raising=False)
+
+
+@pytest.mark.parametrize("dev", [0, 1])
+def test_a_graph_of_any_device_gets_room_of_its_own(monkeypatch, dev):
+    """Also of a device that is not the current one: room of the device whose stream is
+    captured, whatever the current device does."""
+    d = Devices(monkeypatch)
+    kept = mx._room(100, dev)
+    assert mx._room(200, dev) is kept
+    d.capturing = {dev}
+    assert mx._room(100, dev) is not kept and d.made[-1].n == 100 and d.made[-1].device == f"cuda:{dev}"
+    d.capturing = {1 - dev}
+    assert mx._room(100, dev) is kept
+    assert d.current == 0
