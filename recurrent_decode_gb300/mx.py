@@ -3,7 +3,9 @@ product, and a cache of slot states in MXINT8 or MXFP4.
 
 Argument marshalling only.  Calls run on the current stream of the device their
 tensors are on, allocate outputs and workspaces from torch's allocator on that
-stream, and do not synchronise.
+stream, and do not synchronise, but for a device's first MX4Matrix and for making a
+StateCache, which wait for a word or bytes of zeros.  With that matrix made, calls may
+be captured into a graph, a process's first product too.
 """
 from __future__ import annotations
 
@@ -12,7 +14,7 @@ import threading
 
 import torch
 
-from . import EINVAL, ETIMEOUT, RWKV7Error, load_library
+from . import EINVAL, ESTATE, ETIMEOUT, RWKV7Error, load_library
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _FORMATS = {"mxfp4": 0, "mxint8": 1}
@@ -30,9 +32,21 @@ _err: dict[int, torch.Tensor] = {}  # per device: the word in which kernels latc
 _err_lock = threading.Lock()
 
 
+def _capturing(dev: int) -> bool:
+    """Whether the current stream of device `dev` is being captured."""
+    if dev == _current_device():
+        return torch._C._cuda_isCurrentStreamCapturing()  # (which asks for the current device's)
+    with torch.cuda.device(dev):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def _err_word(dev: int) -> torch.Tensor:
+    """Made with the device's first MX4Matrix, or by its first product or check.  Not in a
+    capture, which could not wait for it and whose memory goes with the graph."""
     w = _err.get(dev)
     if w is None:
+        if _capturing(dev):
+            raise RWKV7Error(ESTATE, f"make an MX4Matrix on cuda:{dev} before the first capture of a product there")
         with _err_lock:  # of threads that come at once, the first makes it
             w = _err.get(dev)
             if w is None:
@@ -53,14 +67,6 @@ def _call(fn, dev: int, *args):
             rc = fn(*args, _raw_stream(dev), C.byref(msg))
     if rc:
         raise RWKV7Error(rc, (msg.value or b"").decode())
-
-
-def _capturing(dev: int) -> bool:
-    """Whether the current stream of device `dev` is being captured."""
-    if dev == _current_device():
-        return torch._C._cuda_isCurrentStreamCapturing()  # (which asks for the current device's)
-    with torch.cuda.device(dev):
-        return torch._C._cuda_isCurrentStreamCapturing()
 
 
 def _room(n: int, dev: int) -> torch.Tensor:
@@ -103,6 +109,12 @@ def _bytes(rows: int, cols: int) -> int:
     return (rows + 127 >> 7) * (cols + 255 >> 8) * 17408
 
 
+def _matrix_made(dev: int):
+    """The error word for the products to come, so that the first may be captured."""
+    if dev not in _err and not _capturing(dev):
+        _err_word(dev)
+
+
 class MX4Matrix:
     """An MXFP4 matrix [rows, cols] on the device, in the tile order the product
     reads (rwkv7_mx4_bytes)."""
@@ -115,6 +127,7 @@ class MX4Matrix:
         if data.numel() != _bytes(rows, cols):
             raise ValueError(f"an MXFP4 matrix of {rows} x {cols} takes {_bytes(rows, cols)} bytes, got {data.numel()}")
         self.data, self.rows, self.cols = data, rows, cols
+        _matrix_made(data.get_device())
 
     @property
     def shape(self):
@@ -142,6 +155,7 @@ def mx4_empty(rows: int, cols: int, device) -> MX4Matrix:
     m.data, m.rows, m.cols = torch.empty(_bytes(rows, cols), dtype=torch.uint8, device=device), rows, cols
     if not m.data.is_cuda:
         raise TypeError("an MXFP4 matrix lies on a CUDA device")
+    _matrix_made(m.data.get_device())
     return m
 
 

@@ -1,6 +1,10 @@
 """The microscaled operators where a call goes wrong beside its values: repeated and
 bad indices, entries that nothing was saved to, tensors and graphs on other streams,
 results over their inputs, powers at the ends of their range."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -114,3 +118,47 @@ def test_indices_and_cache_may_be_dropped_at_once(own_stream):
     same(torch.from_numpy(got[0]), nearest(states[2][0], "mxint8"))
     assert (got[2] == states[2][2]).all()
     assert (ctx.get_state(0)[0] == states[0][0]).all()
+
+
+# ------------------------------------------------------------------ graphs
+def fresh_process(code):
+    """What a new process prints that runs `code` after the imports."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", "import torch\nimport recurrent_decode_gb300 as rd\n" + code],
+                       cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    return r.stdout.split()
+
+
+def test_first_product_of_a_process_is_captured():
+    assert fresh_process("""
+x, out = torch.ones(12, 640, device="cuda"), torch.empty(12, 70, device="cuda")
+w = rd.mx4_quantize(torch.ones(70, 640, device="cuda"))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    rd.mx4_linear(x, w, out=out)
+out.zero_()
+g.replay()
+rd.mx4_check()
+print(bool((out == 640).all()))
+""") == ["True"]
+
+
+def test_a_first_matrix_in_a_capture_refuses_the_product_and_leaves_the_capture():
+    assert fresh_process("""
+x, v, out = torch.ones(12, 640, device="cuda"), torch.ones(70, 640, device="cuda"), torch.empty(70, 640, device="cuda")
+rd.load_library()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    w = rd.mx4_quantize(v)
+    try:
+        rd.mx4_linear(x, w)
+    except rd.RWKV7Error as e:
+        print(e.code == rd.ESTATE)
+    w.dequantize(out=out)
+g.replay()
+print(bool((out == 1).all()), bool((rd.mx4_linear(x, rd.mx4_quantize(v)) == 640).all()))
+rd.mx4_check()
+""") == ["True", "True", "True"]

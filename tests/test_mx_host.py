@@ -92,6 +92,7 @@ def test_threads_that_come_at_once_share_one_error_word(monkeypatch):
         time.sleep(0.02)  # long enough for all threads to find no word
         return object()
     monkeypatch.setattr(mx, "_err", {})
+    monkeypatch.setattr(mx, "_capturing", lambda dev: False)
     monkeypatch.setattr(torch, "zeros", zeros)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: SimpleNamespace(synchronize=lambda: None))
     start, words = threading.Barrier(8), []
@@ -150,3 +151,23 @@ def test_a_graph_of_any_device_gets_room_of_its_own(monkeypatch, dev):
     d.capturing = {1 - dev}
     assert mx._room(100, dev) is kept
     assert d.current == 0
+
+
+def test_the_error_word_is_made_with_a_devices_first_matrix(monkeypatch):
+    d = Devices(monkeypatch)
+    monkeypatch.setattr(mx, "_err", {})
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: "word of " + k["device"])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: SimpleNamespace(synchronize=lambda: None))
+    data = SimpleNamespace(is_cuda=True, get_device=lambda: 1)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: data)
+    d.capturing = {1}
+    mx.mx4_empty(1, 32, "cuda:1")  # quantised inside a capture: no word yet
+    assert mx._err == {}
+    with pytest.raises(rd.RWKV7Error, match="before the first capture") as e:
+        mx._err_word(1)
+    assert e.value.code == rd.ESTATE and mx._err == {}
+    d.capturing = {0}
+    mx.mx4_empty(1, 32, "cuda:1")
+    assert mx._err == {1: "word of cuda:1"}
+    d.capturing = {1}
+    assert mx._err_word(1) == "word of cuda:1"
