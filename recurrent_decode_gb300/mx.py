@@ -40,6 +40,12 @@ def _capturing(dev: int) -> bool:
         return torch._C._cuda_isCurrentStreamCapturing()
 
 
+def _word(device) -> torch.Tensor:
+    """A word of zeros that a check may reset, in inference mode or out of it."""
+    with torch.inference_mode(False):
+        return torch.zeros(1, dtype=torch.int32, device=device)
+
+
 def _err_word(dev: int) -> torch.Tensor:
     """Made with the device's first MX4Matrix, or by its first product or check.  Not in a
     capture, which could not wait for it and whose memory goes with the graph."""
@@ -50,7 +56,7 @@ def _err_word(dev: int) -> torch.Tensor:
         with _err_lock:  # of threads that come at once, the first makes it
             w = _err.get(dev)
             if w is None:
-                w = torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
+                w = _word(f"cuda:{dev}")
                 torch.cuda.current_stream(dev).synchronize()  # other streams will use it
                 _err[dev] = w
     return w
@@ -265,7 +271,7 @@ class StateCache:
                                 device="cuda" if device is None else device)
         if not self.data.is_cuda:
             raise TypeError("a state cache lies on a CUDA device")
-        self.err = torch.zeros(1, dtype=torch.int32, device=self.data.device)
+        self.err = _word(self.data.device)
         torch.cuda.current_stream(self.data.device).synchronize()  # a ctx may use it on a stream of its own
 
     def _states(self, fn, states, slots, entries):

@@ -162,3 +162,12 @@ g.replay()
 print(bool((out == 1).all()), bool((rd.mx4_linear(x, rd.mx4_quantize(v)) == 640).all()))
 rd.mx4_check()
 """) == ["True", "True", "True"]
+
+
+def test_a_cache_made_in_inference_mode_is_checked_outside():
+    with torch.inference_mode():
+        cache = rd.StateCache(1, 1, 1)
+        cache.save(tuple(t.cuda() for t in pool(1, 1, 1, 34)), ints(0), ints(1))
+    with pytest.raises(rd.RWKV7Error):
+        cache.check()
+    cache.check()

@@ -171,3 +171,17 @@ def test_the_error_word_is_made_with_a_devices_first_matrix(monkeypatch):
     assert mx._err == {1: "word of cuda:1"}
     d.capturing = {1}
     assert mx._err_word(1) == "word of cuda:1"
+
+
+def test_the_error_word_is_no_inference_tensor(monkeypatch):
+    """It may be made under inference_mode and reset by a check outside."""
+    zeros = torch.zeros
+    monkeypatch.setattr(mx, "_err", {})
+    monkeypatch.setattr(mx, "_capturing", lambda dev: False)
+    monkeypatch.setattr(torch, "zeros", lambda *a, dtype, device: zeros(*a, dtype=dtype))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: SimpleNamespace(synchronize=lambda: None))
+    with torch.inference_mode():
+        w = mx._err_word(0)
+    w.fill_(8)
+    w.zero_()
+    assert not w.is_inference()
