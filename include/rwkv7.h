@@ -381,7 +381,8 @@ RWKV7_API int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols,
  * [B][K] and [N][K], fp32 sums, the result rounded once to y_dtype (row stride
  * ldy elements).  d_x_mx holds x; or, if d_x is not NULL, x is what its rows
  * (x_dtype, row stride ldx) quantise to, and d_x_mx (rwkv7_mx4_bytes(B, K)
- * bytes) is room for it, of unspecified contents afterwards.  B may be 0.  d_err: a device
+ * bytes) is room for it, of unspecified contents afterwards.  y may overlap the rows
+ * d_x, but neither matrix, nor the room w.  B may be 0.  d_err: a device
  * word the caller zeroed; bit 8 is set if a bounded wait in the kernel gave up
  * (y is then undefined). */
 RWKV7_API int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx, int64_t B,

@@ -310,6 +310,34 @@ bool mx_size_ok(int64_t rows, int64_t cols) {
     return rows >= 0 && cols >= 1 && rows <= RWKV7_MX_MAX_DIM && cols <= RWKV7_MX_MAX_DIM;
 }
 
+// Rows in memory: `rows` of `width` bytes, `step` bytes apart (contiguous: one row).
+struct MxSpan {
+    uintptr_t at;
+    uint64_t rows, width, step;
+    MxSpan(const void *p, int64_t r, int64_t cols, int64_t ld, int size)
+        : at((uintptr_t)p), rows((uint64_t)r), width((uint64_t)(cols * size)), step((uint64_t)ld * (uint64_t)size) {
+        if (rows > 1 && step == width) width *= rows, rows = 1;
+    }
+    uintptr_t end() const { return at + (rows - 1) * step * (rows > 1) + width; }
+};
+MxSpan mx_matrix_span(const void *mx, int64_t rows, int64_t cols) {
+    return MxSpan(mx, 1, (int64_t)rwkv7_mx4_bytes(rows, cols), 0, 1);
+}
+// Whether two of them, with rows, share a byte.  Certain where one is contiguous or both
+// have the same step; otherwise true where their ends overlap.
+bool mx_share(const MxSpan &a, const MxSpan &b) {
+    if (a.end() <= b.at || b.end() <= a.at) return false;
+    if (a.rows > 1 && b.rows > 1) {
+        if (a.step != b.step) return true;
+        const uint64_t gap = b.at >= a.at ? (b.at - a.at) % a.step : (a.step - (a.at - b.at) % a.step) % a.step;
+        return gap < a.width || gap + b.width > a.step;  // b's columns against a's, and against a's next row
+    }
+    if (a.rows == 1 && b.rows == 1) return true;
+    const MxSpan &r = a.rows > 1 ? a : b, &c = a.rows > 1 ? b : a;
+    const uint64_t i = c.at < r.at + r.width ? 0 : (c.at - r.at - r.width) / r.step + 1;  // r's first row that ends past c.at
+    return i < r.rows && r.at + i * r.step < c.end();
+}
+
 int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, const void *mx,
                   const char **err_msg) {
     if (err_msg) *err_msg = "";
@@ -441,6 +469,8 @@ int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx
         return mx_fail(err_msg, RWKV7_EINVAL, "the output pointer is not aligned to its type");
     if (((uintptr_t)d_x_mx | (uintptr_t)d_w_mx) & 15u)
         return mx_fail(err_msg, RWKV7_EINVAL, "MXFP4 matrices must be 16-byte aligned");
+    const MxSpan y(d_y, B, N, ldy, y_dtype == RWKV7_F32 ? 4 : 2);
+    const MxSpan x_mx = mx_matrix_span(d_x_mx, B, K), w_mx = mx_matrix_span(d_w_mx, N, K);
     MxLinearParams p;
     memset(&p, 0, sizeof p);
     struct Rows {
@@ -454,7 +484,11 @@ int rwkv7_mx4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, void *d_x_mx
         rows.type = x_dtype;
         rows.stream = static_cast<cudaStream_t>(cuda_stream);
         p.rows = d_x, p.rtype = x_dtype, p.rvec = rows.q.vec, p.ldr = ldx;
+        p.over = mx_share(MxSpan(d_x, B, K, ldx, x_dtype == RWKV7_F32 ? 4 : 2), y);
+        if (mx_share(x_mx, w_mx)) return mx_fail(err_msg, RWKV7_EINVAL, "the room for x overlaps w");
     }
+    if (mx_share(y, x_mx) || mx_share(y, w_mx))
+        return mx_fail(err_msg, RWKV7_EINVAL, "the output overlaps an MXFP4 matrix of the product");
     p.x = static_cast<const uint8_t *>(d_x_mx);
     p.w = static_cast<const uint8_t *>(d_w_mx);
     p.y = d_y;

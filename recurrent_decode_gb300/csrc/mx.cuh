@@ -48,6 +48,7 @@ struct MxLinearParams {
     const uint8_t *x, *w;  // MXFP4 matrices [B][K], [N][K]
     const void *rows;      // if not null, what x is quantised from: rows of type rtype, ldr apart,
     int rtype, rvec;       // rvec: on 16-byte (fp32: 32-byte) boundaries
+    int over;              // they may share memory with y
     int64_t ldr;
     void *y;
     int64_t ldy;

@@ -23,7 +23,9 @@
 //                covers 32 neighbouring outputs
 // Up to 16 rows of x of moderate length are quantised by these warps of every CTA
 // themselves, into shared memory where they stay, while the first weights are on
-// their way.
+// their way.  Not where y shares memory with them: a CTA's y would come under the rows
+// that a later one has still to read.  A kernel of their own reads them all before
+// any y is stored.
 //
 // Each stage has columns of its own for its powers: they are overwritten only
 // after the commit that also frees the stage's shared memory.  A CTA takes all of
@@ -612,7 +614,7 @@ void launch_mx_linear(const MxLinearParams &p, int type, cudaStream_t stream, cu
     uint32_t smem = MXL_SMEM_MAX - 1024;
     a.xres = 0;
     const int kn = ceil_div(a.kt, a.split);
-    if (p.rows && p.B <= 16 && p.B * kn <= MXL_XLINES * MXL_EPI_WARPS && kn <= MXL_XRES) {
+    if (p.rows && !p.over && p.B <= 16 && p.B * kn <= MXL_XLINES * MXL_EPI_WARPS && kn <= MXL_XRES) {
         a.stage_bytes = MX_TILE_BYTES;
         smem -= (uint32_t)kn * MXL_XREC;
         a.xres = smem & ~1023u;

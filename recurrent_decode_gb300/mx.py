@@ -181,8 +181,8 @@ def mx4_linear(x, w: MX4Matrix, out=None, out_dtype=None, activation=None):
     """act(q(x) w^T): x [B, K] (float32, float16, bfloat16, any row stride; quantised
     on the way) or an MX4Matrix [B, K], w an MX4Matrix [N, K]; fp32 sums, the
     result [B, N] rounded once to out's type, or out_dtype (default: x's, float32
-    for an MX4Matrix).  activation: None or "relu2" (max(y, 0)^2).
-    rwkv7_mx4_linear."""
+    for an MX4Matrix).  out may be x or overlap it, but not a matrix.  activation: None
+    or "relu2" (max(y, 0)^2).  rwkv7_mx4_linear."""
     if not isinstance(w, MX4Matrix):
         raise TypeError("w must be an MX4Matrix")
     act = _ACTIVATIONS.get(activation)

@@ -171,3 +171,49 @@ def test_a_cache_made_in_inference_mode_is_checked_outside():
     with pytest.raises(rd.RWKV7Error):
         cache.check()
     cache.check()
+
+
+# ------------------------------------------------------------------ results over their inputs
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("B,K", [(1, 700), (3, 2560), (16, 640), (16, 2560), (17, 640), (130, 640)])
+def test_a_product_over_its_own_rows(B, K, dtype):
+    """out = x, out shifted against x in one buffer, and rows of a different step: as
+    into memory of its own, whether few rows or many."""
+    w = rd.mx4_quantize((torch.randn(K, K, generator=cpu(K)) * 0.05).cuda())
+    x = torch.randn(B, K, generator=cpu(B)).to(dtype).cuda()
+    want = rd.mx4_linear(x, w, activation="relu2")
+    for shift, step in ((0, K), (8, K), (5, K), (3, K + 9)):
+        flat = torch.zeros(B * (K + 9) + 64, dtype=dtype, device="cuda")
+        rows, out = torch.as_strided(flat, (B, K), (K, 1), 0), torch.as_strided(flat, (B, K), (step, 1), shift)
+        rows.copy_(x)
+        assert torch.equal(rd.mx4_linear(rows, w, out=out, activation="relu2"), want)
+    rd.mx4_check()
+
+
+@pytest.mark.parametrize("B", [1, 4, 16, 40])
+def test_a_product_beside_its_rows_in_one_buffer(B):
+    w = rd.mx4_quantize(torch.randn(96, 300, generator=cpu(1)).cuda())
+    both = torch.randn(B, 500, generator=cpu(B)).cuda()
+    x = both[:, 7:307].clone()
+    want = rd.mx4_linear(x, w)
+    assert torch.equal(rd.mx4_linear(both[:, 7:307], w, out=both[:, 307:403]), want)
+    assert torch.equal(both[:, 7:307], x)
+
+
+def test_a_product_may_write_between_and_around_its_matrices():
+    """Rows of y 32 KB apart with the matrices between them; over them it is refused."""
+    flat = torch.zeros(6 << 15, dtype=torch.uint8, device="cuda")
+    at = lambda k: flat[(k << 15) + 64:][:17408]  # noqa: E731
+    x, v = torch.randn(5, 64, generator=cpu(2)).cuda(), torch.randn(32, 64, generator=cpu(3)).cuda()
+    w, xq = rd.MX4Matrix(at(1), 32, 64), rd.MX4Matrix(at(3), 5, 64)
+    rd.mx4_quantize(v, out=w), rd.mx4_quantize(x, out=xq)
+    want = rd.mx4_linear(x, rd.mx4_quantize(v), out_dtype=torch.float16)
+    out = torch.as_strided(flat.view(torch.float16), (5, 32), (1 << 14, 1), 0)
+    assert torch.equal(rd.mx4_linear(xq, w, out=out), want)
+    assert torch.equal(rd.mx4_linear(x, w, out=out), want)
+    for shift in (1, 32, 8000):
+        bad = torch.as_strided(flat.view(torch.float16), (5, 32), (1 << 14, 1), shift)
+        for rows in (x, xq):
+            with pytest.raises(rd.RWKV7Error, match="overlaps"):
+                rd.mx4_linear(rows, w, out=bad)
+    assert torch.equal(rd.mx4_linear(xq, xq), rd.mx4_linear(x, rd.mx4_quantize(x)))  # one matrix on both sides

@@ -1,6 +1,7 @@
 """What the binding of the microscaled operators does on the host: the order of streams,
 the memory that calls keep, who makes the error word, indices of the packed prefix
 cache.  No GPU: the library, streams and tensors are stand-ins."""
+import ctypes as C
 from types import SimpleNamespace
 
 import pytest
@@ -185,3 +186,27 @@ def test_the_error_word_is_no_inference_tensor(monkeypatch):
     w.fill_(8)
     w.zero_()
     assert not w.is_inference()
+
+
+# ------------------------------------------------------------------ memory that calls share
+def refused(fn, *args):
+    msg = C.c_char_p(b"unset")
+    assert fn(*args, None, C.byref(msg)) == rd.EINVAL
+    return msg.value.decode()
+
+
+def test_a_product_refuses_to_write_over_its_matrices():
+    """x 2 x 64 fp16 rows 128 apart from 1 << 20, room for them (one tile) from 2 << 20,
+    w (8 x 64, one tile) from 3 << 20, y 2 x 8 fp16 rows 8 apart from 4 << 20."""
+    rd.build()
+    f = rd.load_library().rwkv7_mx4_linear
+    X, ROOM, W, Y, TILE = 1 << 20, 2 << 20, 3 << 20, 4 << 20, 17408
+
+    def call(x=X, room=ROOM, w=W, y=Y, ldy=8, B=2):
+        return x, 1, 128, room, B, w, 8, 64, y, 1, ldy, 0, 8 << 20
+    for bad in (dict(y=W), dict(y=W + TILE - 2), dict(y=W - 30), dict(y=ROOM), dict(y=ROOM + TILE - 16),
+                dict(x=None, y=ROOM), dict(y=W - 4096 - 14, ldy=2048), dict(y=W - 4096 + 16, ldy=2048),
+                dict(y=W - 10 * 65536 + TILE - 2, ldy=32768, B=11)):
+        assert "output overlaps" in refused(f, *call(**bad))
+    for bad in (dict(room=W), dict(room=W - TILE + 16), dict(room=W + TILE - 16)):
+        assert "room" in refused(f, *call(**bad))
