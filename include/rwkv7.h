@@ -367,13 +367,13 @@ RWKV7_API size_t rwkv7_mx4_bytes(int64_t rows, int64_t cols);
 
 /* Quantise rows: d_x [rows][cols] of type dtype (RWKV7_F32 / F16 / BF16), row
  * stride ld elements (any; rows that start on 16-byte boundaries are read
- * fastest), into d_mx (rwkv7_mx4_bytes(rows, cols) bytes, 16-byte aligned).
- * rows may be 0. */
+ * fastest), into d_mx (rwkv7_mx4_bytes(rows, cols) bytes, 16-byte aligned, not over
+ * the rows).  rows may be 0. */
 RWKV7_API int rwkv7_mx4_quantize(const void *d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                                  void *d_mx, void *cuda_stream, const char **err_msg);
 
 /* The values an MXFP4 matrix stands for, rounded to dtype (exact in fp32 and,
- * inside its range, in fp16 and bf16), into d_y at row stride ld. */
+ * inside its range, in fp16 and bf16), into d_y at row stride ld, not over the matrix. */
 RWKV7_API int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y, int32_t dtype,
                                    int64_t ld, void *cuda_stream, const char **err_msg);
 

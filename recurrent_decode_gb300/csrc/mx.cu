@@ -357,6 +357,8 @@ int mx_rows_check(MxRowsParams &p, const void *x, int32_t dtype, int64_t rows, i
     p.kt = (int)((cols + MX_TILE_K - 1) / MX_TILE_K);
     if (rows > (INT32_MAX - 4096) / p.kt)
         return mx_fail(err_msg, RWKV7_EINVAL, "%lld rows of %lld columns are too many", rows, cols);
+    if (rows > 0 && mx_share(MxSpan(x, rows, cols, ld, size), mx_matrix_span(mx, rows, cols)))
+        return mx_fail(err_msg, RWKV7_EINVAL, "the rows and the MXFP4 matrix overlap");
     p.rows = (int)rows;
     const int step = 8 * size;  // bytes of a lane's eight values
     p.vec = (uintptr_t)x % step == 0 && (rows <= 1 || ld * size % step == 0);

@@ -217,3 +217,13 @@ def test_a_product_may_write_between_and_around_its_matrices():
             with pytest.raises(rd.RWKV7Error, match="overlaps"):
                 rd.mx4_linear(rows, w, out=bad)
     assert torch.equal(rd.mx4_linear(xq, xq), rd.mx4_linear(x, rd.mx4_quantize(x)))  # one matrix on both sides
+
+
+def test_rows_may_lie_around_their_matrix():
+    """Rows 32 KB apart with their matrix between them."""
+    flat = torch.zeros(3 << 15, dtype=torch.uint8, device="cuda")
+    x = torch.as_strided(flat.view(torch.float32), (3, 40), (1 << 13, 1), 5)
+    x.copy_(torch.randn(3, 40, generator=cpu(4)))
+    want = nearest(x.double().cpu().numpy(), "mxfp4")
+    m = rd.mx4_quantize(x, out=rd.MX4Matrix(flat[1024:1024 + 17408], 3, 40))
+    same(m.dequantize(out=x), want)

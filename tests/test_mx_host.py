@@ -210,3 +210,14 @@ def test_a_product_refuses_to_write_over_its_matrices():
         assert "output overlaps" in refused(f, *call(**bad))
     for bad in (dict(room=W), dict(room=W - TILE + 16), dict(room=W + TILE - 16)):
         assert "room" in refused(f, *call(**bad))
+
+
+def test_rows_and_their_matrix_do_not_overlap():
+    """Four fp32 rows of 32 values and a matrix of one tile."""
+    rd.build()
+    lib, M, TILE = rd.load_library(), 1 << 20, 17408
+    for x, ld in ((M, 32), (M - 508, 32), (M + TILE - 4, 32), (M - 3 * 8192 - 124, 2048), (M - 8192 + 64, 2048)):
+        assert "overlap" in refused(lib.rwkv7_mx4_quantize, x, 0, 4, 32, ld, M)
+        assert "overlap" in refused(lib.rwkv7_mx4_dequantize, M, 4, 32, x, 0, ld)
+    # the room for x
+    assert "overlap" in refused(lib.rwkv7_mx4_linear, M, 0, 32, M, 4, 2 * M, 8, 32, 3 * M, 0, 8, 0, 4 * M)
