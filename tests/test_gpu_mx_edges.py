@@ -227,3 +227,17 @@ def test_rows_may_lie_around_their_matrix():
     want = nearest(x.double().cpu().numpy(), "mxfp4")
     m = rd.mx4_quantize(x, out=rd.MX4Matrix(flat[1024:1024 + 17408], 3, 40))
     same(m.dequantize(out=x), want)
+
+
+def test_room_is_kept_for_torchs_own_streams_only():
+    from recurrent_decode_gb300 import mx
+    w, x = rd.mx4_quantize(torch.ones(70, 640, device="cuda")), torch.ones(40, 640, device="cuda")
+    own = [torch.cuda.default_stream(), torch.cuda.Stream(), torch.cuda.Stream(priority=-1)]
+    torch.cuda.synchronize()
+    for i, s in enumerate(own + [torch.cuda.ExternalStream(own[1].cuda_stream)]):
+        vars(mx._kept).clear()
+        with torch.cuda.stream(s):
+            y = rd.mx4_linear(x, w)
+        s.synchronize()
+        assert bool((y == 640).all()) and len(vars(mx._kept)) == (1 if i < len(own) else 0)
+    rd.mx4_check()

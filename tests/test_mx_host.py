@@ -134,6 +134,7 @@ class Devices:
         monkeypatch.setattr(mx, "_kept", SimpleNamespace())
         monkeypatch.setattr(mx, "_current_device", lambda: self.current)
         monkeypatch.setattr(mx, "_raw_stream", lambda dev: self.stream[dev])
+        monkeypatch.setattr(mx, "_stream_data", lambda dev: (self.stream[dev], dev, 1), raising=False)
         monkeypatch.setattr(torch.cuda, "device", device)
         monkeypatch.setattr(torch, "empty", empty)
         monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: self.current in self.capturing,
@@ -221,3 +222,18 @@ def test_rows_and_their_matrix_do_not_overlap():
         assert "overlap" in refused(lib.rwkv7_mx4_dequantize, M, 4, 32, x, 0, ld)
     # the room for x
     assert "overlap" in refused(lib.rwkv7_mx4_linear, M, 0, 32, M, 4, 2 * M, 8, 32, 3 * M, 0, 8, 0, 4 * M)
+
+
+def test_room_is_kept_for_streams_that_cannot_be_destroyed(monkeypatch):
+    """By stream, for torch's own; a handle that came from elsewhere may be another
+    stream's by the next call."""
+    d = Devices(monkeypatch)
+    first = mx._room(100, 0)
+    d.stream[0] = 3
+    second = mx._room(100, 0)
+    assert second is not first and mx._room(100, 0) is second
+    d.stream[0] = 0
+    assert mx._room(100, 0) is first
+    d.stream[0] = 0x5580_1234_5670
+    a, b = mx._room(100, 0), mx._room(100, 0)
+    assert a is not b and a.n == b.n == 100 and not any(k[1] == d.stream[0] for k in vars(mx._kept))
