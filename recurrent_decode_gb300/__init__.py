@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from importlib.util import find_spec
 
 import numpy as np
 
@@ -438,5 +439,10 @@ def __getattr__(name):
     return globals()[name]
 
 
-__all__ = [*_MX, "Rwkv7", "RWKV7Error", "Config", "Sampling", "load_library", "build", "LIB_PATH",
-           "SIGNATURES", "MAX_STEP_BATCH", "PROF_CLASSES", "set_device_allocator"]
+def __dir__():
+    return sorted({*globals(), *_MX})
+
+
+# A star import looks every name up: _MX only where there is a torch to import with them.
+__all__ = [*(_MX if find_spec("torch") else ()), "Rwkv7", "RWKV7Error", "Config", "Sampling", "load_library", "build",
+           "LIB_PATH", "SIGNATURES", "MAX_STEP_BATCH", "PROF_CLASSES", "set_device_allocator"]

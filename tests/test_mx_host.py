@@ -2,6 +2,9 @@
 the memory that calls keep, who makes the error word, indices of the packed prefix
 cache.  No GPU: the library, streams and tensors are stand-ins."""
 import ctypes as C
+import os
+import subprocess
+import sys
 from types import SimpleNamespace
 
 import pytest
@@ -237,3 +240,27 @@ def test_room_is_kept_for_streams_that_cannot_be_destroyed(monkeypatch):
     d.stream[0] = 0x5580_1234_5670
     a, b = mx._room(100, 0), mx._room(100, 0)
     assert a is not b and a.n == b.n == 100 and not any(k[1] == d.stream[0] for k in vars(mx._kept))
+
+
+# ------------------------------------------------------------------ imports
+def test_a_star_import_needs_no_torch():
+    """Nor do the package and its names outside the microscaled operators, which are
+    there on first use and listed by dir()."""
+    code = """
+import sys
+sys.modules["torch"] = None  # an import of it raises
+from recurrent_decode_gb300 import *
+import recurrent_decode_gb300 as rd
+assert Rwkv7 is rd.Rwkv7 and "mx4_linear" in dir(rd) and "Rwkv7" in dir(rd)
+try:
+    rd.mx4_linear
+except ImportError:
+    print("no torch")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == ["no", "torch"]
+    names = {}
+    exec("from recurrent_decode_gb300 import *", names)  # here there is one
+    assert all(names[n] is getattr(mx, n) for n in rd._MX)
