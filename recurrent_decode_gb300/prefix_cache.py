@@ -98,12 +98,13 @@ class PrefixStateCache:
         if k in self.entries:
             self.entries.move_to_end(k)
             return
+        slot = self.free[-1] if self.free else next(iter(self.entries.values()))
+        self._put(src_slot, slot)  # if it is refused, the cache is as it was
         if self.free:
-            slot = self.free.pop()
+            self.free.pop()
         else:
-            _, slot = self.entries.popitem(last=False)
+            self.entries.popitem(last=False)
             self.evictions += 1
-        self._put(src_slot, slot)
         self.entries[k] = slot
         self.stores += 1
 

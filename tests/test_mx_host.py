@@ -7,11 +7,13 @@ import subprocess
 import sys
 from types import SimpleNamespace
 
+import numpy as np
 import pytest
 import torch
 
 import recurrent_decode_gb300 as rd
 from recurrent_decode_gb300 import mx
+from recurrent_decode_gb300.prefix_cache import PrefixStateCache
 
 CUDA0, CUDA1 = torch.device("cuda", 0), torch.device("cuda", 1)
 
@@ -264,3 +266,37 @@ except ImportError:
     names = {}
     exec("from recurrent_decode_gb300 import *", names)  # here there is one
     assert all(names[n] is getattr(mx, n) for n in rd._MX)
+
+
+# ------------------------------------------------------------------ prefix caches
+class Slots:
+    """A context of two slots that refuses others, as the library does."""
+    n_slots, dims, stream = 2, SimpleNamespace(n_layer=2, n_head=3), SimpleNamespace(device=CUDA1)
+
+    def __init__(self):
+        self.calls = []
+
+    def slot_copy(self, src, dst):
+        if not 0 <= src < self.n_slots + 2:
+            raise rd.RWKV7Error(rd.EINVAL, "slot out of range")
+        self.calls.append((src, dst))
+
+
+def contents(cache):
+    return (list(cache.entries.items()), list(cache.free), cache.hits, cache.misses, cache.hit_tokens, cache.stores,
+            cache.evictions)
+
+
+def test_a_refused_store_leaves_the_prefix_cache_as_it_was():
+    cache = PrefixStateCache(Slots(), [2, 3], block=4)
+    a, b, c = (np.full(4, i, np.int32) for i in range(3))
+    for have in (a, b, None):  # with two free slots, with one, with none
+        before = contents(cache)
+        with pytest.raises(rd.RWKV7Error):
+            cache.store(c, 9)
+        assert contents(cache) == before
+        if have is not None:
+            cache.store(have, 0)
+    assert len(cache) == 2 and cache.lookup(a)[0] == 4 and cache.lookup(c)[0] == 0
+    cache.store(c, 1)
+    assert cache.evictions == 1 and cache.lookup(b)[0] == 0 and cache.lookup(c)[0] == 4
