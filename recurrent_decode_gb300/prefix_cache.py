@@ -25,7 +25,7 @@ from collections import OrderedDict
 
 import numpy as np
 
-from . import MAX_STEP_BATCH
+from . import EINVAL, MAX_STEP_BATCH, RWKV7Error
 
 
 def _key(tokens: np.ndarray) -> bytes:
@@ -139,8 +139,15 @@ class PackedPrefixStateCache(PrefixStateCache):
         self._index = torch.arange(max(n_entries, ctx.n_slots), dtype=torch.int32, device=self.states.data.device)
         torch.cuda.current_stream(self._index.device).synchronize()  # the ctx reads it on its own stream
 
+    def _slot(self, slot: int):
+        """A slot as the device index the ctx reads; refused out of range, as slot_copy
+        does, before the host counts on the copy."""
+        if not 0 <= slot < self.ctx.n_slots:
+            raise RWKV7Error(EINVAL, f"slot {slot} out of range")
+        return self._index[slot:slot + 1]
+
     def _put(self, src_slot: int, entry: int) -> None:
-        self.ctx.slots_save(self.states, self._index[src_slot:src_slot + 1], self._index[entry:entry + 1])
+        self.ctx.slots_save(self.states, self._slot(src_slot), self._index[entry:entry + 1])
 
     def _get(self, entry: int, dst_slot: int) -> None:
-        self.ctx.slots_load(self.states, self._index[entry:entry + 1], self._index[dst_slot:dst_slot + 1])
+        self.ctx.slots_load(self.states, self._index[entry:entry + 1], self._slot(dst_slot))

@@ -13,7 +13,7 @@ import torch
 
 import recurrent_decode_gb300 as rd
 from recurrent_decode_gb300 import mx
-from recurrent_decode_gb300.prefix_cache import PrefixStateCache
+from recurrent_decode_gb300.prefix_cache import PackedPrefixStateCache, PrefixStateCache
 
 CUDA0, CUDA1 = torch.device("cuda", 0), torch.device("cuda", 1)
 
@@ -300,3 +300,43 @@ def test_a_refused_store_leaves_the_prefix_cache_as_it_was():
     assert len(cache) == 2 and cache.lookup(a)[0] == 4 and cache.lookup(c)[0] == 0
     cache.store(c, 1)
     assert cache.evictions == 1 and cache.lookup(b)[0] == 0 and cache.lookup(c)[0] == 4
+
+
+class PackedSlots(Slots):
+    """Moves states as the device does, which leaves a pair out of range out and says so later."""
+
+    def slots_save(self, cache, slots, entries):
+        self.calls.append(("save", slots.tolist(), entries.tolist()))
+
+    def slots_load(self, cache, entries, slots):
+        self.calls.append(("load", entries.tolist(), slots.tolist()))
+
+
+@pytest.fixture
+def packed(monkeypatch):
+    """A packed prefix cache of six entries over a context of two slots."""
+    made = []
+
+    def state_cache(n_layer, n_head, n_entries, format="mxint8", device=None):
+        made.append((n_layer, n_head, n_entries, format, device))
+        return SimpleNamespace(data=SimpleNamespace(device="cpu"))
+    monkeypatch.setattr(mx, "StateCache", state_cache)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(synchronize=lambda: None))
+    cache = PackedPrefixStateCache(PackedSlots(), 6, "mxfp4", block=4)
+    cache.made = made
+    return cache
+
+
+@pytest.mark.parametrize("slot", [-1, 2, 5, 6])
+def test_packed_prefix_cache_refuses_a_slot_out_of_range(packed, slot):
+    """Also one that is an entry's number, at storing and at restoring."""
+    a = np.arange(4, dtype=np.int32)
+    packed.store(a, 1)
+    assert packed.restore(a, 0) == 4
+    assert packed.ctx.calls == [("save", [1], [5]), ("load", [5], [0])]
+    before = contents(packed)
+    for call in (lambda: packed.store(a + 1, slot), lambda: packed.restore(a, slot)):
+        with pytest.raises(rd.RWKV7Error, match="out of range") as e:
+            call()
+        assert e.value.code == rd.EINVAL
+    assert contents(packed) == before and len(packed.ctx.calls) == 2 and packed.lookup(a + 1)[0] == 0
