@@ -135,7 +135,7 @@ class PackedPrefixStateCache(PrefixStateCache):
         import torch
 
         from .mx import StateCache
-        self.states = StateCache(ctx.dims.n_layer, ctx.dims.n_head, n_entries, format)
+        self.states = StateCache(ctx.dims.n_layer, ctx.dims.n_head, n_entries, format, ctx.stream.device)
         self._index = torch.arange(max(n_entries, ctx.n_slots), dtype=torch.int32, device=self.states.data.device)
         torch.cuda.current_stream(self._index.device).synchronize()  # the ctx reads it on its own stream
 

@@ -340,3 +340,7 @@ def test_packed_prefix_cache_refuses_a_slot_out_of_range(packed, slot):
             call()
         assert e.value.code == rd.EINVAL
     assert contents(packed) == before and len(packed.ctx.calls) == 2 and packed.lookup(a + 1)[0] == 0
+
+
+def test_packed_prefix_cache_lies_on_the_contexts_device(packed):
+    assert packed.made == [(2, 3, 6, "mxfp4", CUDA1)]
