@@ -819,8 +819,9 @@ void launch_lora_fin(const LoraFinParams &p, const LaunchCfg &lc, cudaError_t *e
 }
 
 void launch_slot_op(const SlotOpParams &p, cudaStream_t s, cudaError_t *e) {
-    slot_op_kernel<<<304, 256, 0, s>>>(p);
-    cudaError_t r = cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = mkcfg(dim3(304), dim3(256), 0, LaunchCfg{s, false}, at);
+    cudaError_t r = cudaLaunchKernelEx(&cfg, slot_op_kernel, p);  // this launch's error, no earlier call's
     if (r != cudaSuccess) *e = r;
 }
 

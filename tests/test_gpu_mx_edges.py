@@ -241,3 +241,30 @@ def test_room_is_kept_for_torchs_own_streams_only():
         s.synchronize()
         assert bool((y == 640).all()) and len(vars(mx._kept)) == (1 if i < len(own) else 0)
     rd.mx4_check()
+
+
+def test_a_refused_launch_leaves_no_error_for_a_slot_call():
+    """A call on a stream whose capture broke says so; the next slot call, on a sound
+    stream, has no part in it."""
+    assert fresh_process("""
+import synth
+ctx = rd.Rwkv7(synth.Dims("tiny"), 2)
+x = torch.ones(4, 64, device="cuda")
+m = rd.mx4_quantize(x)
+torch.cuda.synchronize()
+try:
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        try:
+            torch.cuda.current_stream().synchronize()
+        except RuntimeError:
+            print("broken")
+        try:
+            rd.mx4_quantize(x, out=m)
+        except rd.RWKV7Error as e:
+            print(e.code == rd.ECUDA)
+except RuntimeError:
+    pass
+ctx.slot_reset(0)
+ctx.synchronize()
+print("reset")
+""") == ["broken", "True", "reset"]
