@@ -5,13 +5,14 @@ import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
 import recurrent_decode_gb300 as rd
 import synth
 from _mx_reference import nearest
-from test_gpu_mx import cpu, ints, pool, same
+from test_gpu_mx import cpu, ints, pool, product, same
 
 pytestmark = pytest.mark.gpu
 
@@ -268,3 +269,73 @@ ctx.slot_reset(0)
 ctx.synchronize()
 print("reset")
 """) == ["broken", "True", "reset"]
+
+
+# ------------------------------------------------------------------ ends of the range
+ENDS = [-127, -126, -100, -64, -1, 0, 63, 101, 124, 125]  # 6 * 2^125 is in fp32's range, 6 * 2^126 is not
+
+
+def powers_apart(x_power, w_power, B=70, N=150):
+    """Rows on the grid in blocks of these powers (a 6 in each pins its power), their exact
+    values in fp64."""
+    g = cpu(50)
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
+    out = []
+    for rows, power in ((B, x_power), (N, w_power)):
+        v = grid[torch.randint(0, 8, (rows, 32 * len(power)), generator=g)]
+        v *= torch.randint(0, 2, v.shape, generator=g) * 2 - 1
+        v[:, ::32] = 6.0
+        out.append(v * 2.0 ** torch.tensor(power, dtype=torch.float64).repeat_interleave(32))
+    return out
+
+
+@pytest.mark.parametrize("B", [3, 70])
+def test_product_of_powers_at_both_ends(B):
+    """Blocks of x from 2^-127 to 2^125 against blocks of w of about the inverse: terms of
+    ordinary size, their sum as exact as the product's always is."""
+    x, w = powers_apart(ENDS, [min(125, -e) for e in ENDS], B)
+    assert torch.equal(x.float().double(), x) and torch.equal(w.float().double(), w)
+    wq, xq = rd.mx4_quantize(w.float().cuda()), rd.mx4_quantize(x.float().cuda())
+    assert torch.equal(wq.dequantize().cpu().double(), w) and torch.equal(xq.dequantize().cpu().double(), x)
+    want, off = product(x.numpy(), w.numpy(), None, torch.float32)
+    for rows in (x.float().cuda(), xq):
+        y = rd.mx4_linear(rows, wq)
+        assert (np.abs(y.double().cpu().numpy() - want) <= off).all()
+    rd.mx4_check()
+
+
+@pytest.mark.parametrize("e", [(-127, -127), (-100, -60), (-75, -70), (-127, -1)])
+def test_products_below_the_normal_range(e):
+    """Within fp32's smallest normal number of the sum, which the bound has in it."""
+    x, w = powers_apart([e[0]] * 3, [e[1]] * 3)
+    want, off = product(x.numpy(), w.numpy(), None, torch.float32)
+    y = rd.mx4_linear(x.float().cuda(), rd.mx4_quantize(w.float().cuda()))
+    assert (np.abs(y.double().cpu().numpy() - want) <= off).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_products_past_the_range_are_infinite(dtype):
+    x, w = powers_apart([70] * 2, [70] * 2)
+    y = rd.mx4_linear(x.abs().float().cuda(), rd.mx4_quantize(w.abs().float().cuda()), out_dtype=dtype)
+    assert bool((y == float("inf")).all())
+    y = rd.mx4_linear(-x.abs().float().cuda(), rd.mx4_quantize(w.abs().float().cuda()), out_dtype=dtype)
+    assert bool((y == float("-inf")).all())
+
+
+@pytest.mark.parametrize("fmt,part", [("mxint8", 127), ("mxfp4", 5)])
+def test_a_state_keeps_its_documented_part(fmt, part):
+    """MXINT8: max > 127/64 * 2^(e-1), so half a step, 2^e/128, is below max/127.  MXFP4:
+    a value is off by 1/4 at most below 2, by 1/2 at 2.5 and by 1 at 5 (times 2^e), each
+    time no more than a fifth of itself or of max > 3 * 2^e.  Down to 2^-126, where e no
+    longer follows max, and at the ties themselves."""
+    st = tuple(t.cuda() for t in pool(1, 2, 2, 35))
+    st[0][0, 0, 0, 0, :32] = 5.0 * 2.0 ** -127  # 5 = a tie between 4 and 6
+    st[0][0, 0, 0, 1, :32] = 2.0 ** -126
+    st[0][0, 0, 0, 2, :32] = torch.linspace(1, 5, 32, device="cuda") * 2.0 ** 100
+    st[0][0, 0, 0, 3, :32] = 3.4 * 2.0 ** 126
+    before = st[0][:, 0].double()
+    cache = rd.StateCache(1, 2, 1, fmt)
+    cache.save(st, ints(0), ints(0))
+    cache.load(st, ints(0), ints(1))
+    d = (st[0][:, 1].double() - before).view(-1, 32).abs().amax(1)
+    assert bool((d * part <= before.view(-1, 32).abs().amax(1)).all())
