@@ -193,13 +193,12 @@ __host__ __device__ constexpr int64_t mx_codes(int64_t heads, int fmt) {
 // earlier pair that writes the same target (one of two copies into the same place
 // would win by chance: the first does, the others are reported).  A pair whose other
 // index is out of range writes nothing, so it makes no later one a repeat.
-__device__ __forceinline__ bool mx_pair_ok(const int32_t *target, int ntarget, const int32_t *other, int nother, int i,
-                                           uint32_t *err, bool speak) {
-    const int32_t t = target[i];
-    int dup = 0;
-    for (int j = threadIdx.x; j < i; j += MXS_THREADS) dup |= target[j] == t && (uint32_t)other[j] < (uint32_t)nother;
+__device__ __forceinline__ bool mx_pair_ok(const int32_t *target, int32_t t, int ntarget, const int32_t *other, int32_t o,
+                                           int nother, int i, uint32_t *err, bool speak) {
+    int dup = 0;  // both loads of a pair at once: with the second only where the first is met, 0.2 us more
+    for (int j = threadIdx.x; j < i; j += MXS_THREADS) dup |= (target[j] == t) & ((uint32_t)other[j] < (uint32_t)nother);
     dup = __syncthreads_or(dup);
-    const bool in = t >= 0 && t < ntarget && (uint32_t)other[i] < (uint32_t)nother;
+    const bool in = (uint32_t)t < (uint32_t)ntarget && (uint32_t)o < (uint32_t)nother;
     if (speak && threadIdx.x == 0 && (dup || !in)) atomicOr(err, in ? ERR_DUP : ERR_SLOT);
     return in && !dup;
 }
@@ -210,8 +209,8 @@ __global__ void __launch_bounds__(MXS_THREADS) mx_state_kernel(const MxStatePara
     const int hl = blockIdx.x, i = blockIdx.y;
     const int layer = hl / p.H, head = hl % p.H;
     const int32_t slot = p.slots[i], entry = p.entries[i];
-    if (!(SAVE ? mx_pair_ok(p.entries, p.n_entries, p.slots, p.n_slots, i, p.err, hl == 0)
-               : mx_pair_ok(p.slots, p.n_slots, p.entries, p.n_entries, i, p.err, hl == 0)))
+    if (!(SAVE ? mx_pair_ok(p.entries, entry, p.n_entries, p.slots, slot, p.n_slots, i, p.err, hl == 0)
+               : mx_pair_ok(p.slots, slot, p.n_slots, p.entries, entry, p.n_entries, i, p.err, hl == 0)))
         return;
     const int64_t heads = (int64_t)p.L * p.H;
     uint8_t *at = p.cache + (int64_t)entry * p.entry_bytes;
