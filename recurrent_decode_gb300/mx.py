@@ -26,9 +26,10 @@ _MAX_DIM = 1 << 24  # RWKV7_MX_MAX_DIM
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _stream_data = torch._C._cuda_getCurrentStream  # (id, ...)
+_is_capturing = torch._C._cuda_isCurrentStreamCapturing  # of the current device
 
 _ROOM = 2 << 20  # 128 rows of 30,000 columns
-_kept = threading.local()  # (device, stream id) -> bytes of _room
+_kept = threading.local()  # (device, stream) -> bytes of _room
 _err: dict[int, torch.Tensor] = {}  # per device: the word in which kernels latch errors
 _err_lock = threading.Lock()
 
@@ -36,9 +37,9 @@ _err_lock = threading.Lock()
 def _capturing(dev: int) -> bool:
     """Whether the current stream of device `dev` is being captured."""
     if dev == _current_device():
-        return torch._C._cuda_isCurrentStreamCapturing()  # (which asks for the current device's)
+        return _is_capturing()
     with torch.cuda.device(dev):
-        return torch._C._cuda_isCurrentStreamCapturing()
+        return _is_capturing()
 
 
 def _word(device) -> torch.Tensor:
@@ -81,17 +82,20 @@ def _room(n: int, dev: int) -> torch.Tensor:
     call of the same host thread on the same stream, whose kernels run after this
     call's (an allocation between two launches costs 3 us, a small product takes 6):
     2 MB for each of torch's streams that a thread makes products on, until it ends.
-    Torch's own streams live as long as the process: the default one, id 0, and those of
-    its pool, whose ids are odd.  One that was made elsewhere, whose id is its handle,
-    may be destroyed with a product in flight and its handle go to another, so it gets
-    bytes of the call's own; and so does a graph."""
-    stream = _stream_data(dev)[0]
-    if n > _ROOM or stream and not stream & 1 or _capturing(dev):
+    Torch's own streams live as long as the process, so their handles stay theirs: the
+    default one, id 0, and those of its pool, whose ids are odd.  One that was made
+    elsewhere, whose id is its handle, may be destroyed with a product in flight and the
+    handle go to another, so it gets bytes of the call's own; and so does a graph."""
+    if n > _ROOM or (_is_capturing() if dev == _current_device() else _capturing(dev)):
         return torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
+    key = dev, _raw_stream(dev)
     rooms = _kept.__dict__
-    w = rooms.get((dev, stream))
+    w = rooms.get(key)
     if w is None:
-        w = rooms[dev, stream] = torch.empty(_ROOM, dtype=torch.uint8, device=f"cuda:{dev}")
+        stream = _stream_data(dev)[0]
+        if stream and not stream & 1:
+            return torch.empty(n, dtype=torch.uint8, device=f"cuda:{dev}")
+        w = rooms[key] = torch.empty(_ROOM, dtype=torch.uint8, device=f"cuda:{dev}")
     return w
 
 

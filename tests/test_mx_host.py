@@ -139,11 +139,10 @@ class Devices:
         monkeypatch.setattr(mx, "_kept", SimpleNamespace())
         monkeypatch.setattr(mx, "_current_device", lambda: self.current)
         monkeypatch.setattr(mx, "_raw_stream", lambda dev: self.stream[dev])
-        monkeypatch.setattr(mx, "_stream_data", lambda dev: (self.stream[dev], dev, 1), raising=False)
+        monkeypatch.setattr(mx, "_stream_data", lambda dev: (self.stream[dev], dev, 1))
         monkeypatch.setattr(torch.cuda, "device", device)
         monkeypatch.setattr(torch, "empty", empty)
-        monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: self.current in self.capturing,
-                            raising=False)
+        monkeypatch.setattr(mx, "_is_capturing", lambda: self.current in self.capturing)
 
 
 @pytest.mark.parametrize("dev", [0, 1])
