@@ -372,8 +372,9 @@ RWKV7_API size_t rwkv7_mx4_bytes(int64_t rows, int64_t cols);
 RWKV7_API int rwkv7_mx4_quantize(const void *d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                                  void *d_mx, void *cuda_stream, const char **err_msg);
 
-/* The values an MXFP4 matrix stands for, rounded to dtype (exact in fp32 and,
- * inside its range, in fp16 and bf16), into d_y at row stride ld, not over the matrix. */
+/* The values an MXFP4 matrix stands for, rounded to dtype (exact inside its range;
+ * 2^128 and more, to which values from 7/8 of fp32's range on may go, are
+ * infinity), into d_y at row stride ld, not over the matrix. */
 RWKV7_API int rwkv7_mx4_dequantize(const void *d_mx, int64_t rows, int64_t cols, void *d_y, int32_t dtype,
                                    int64_t ld, void *cuda_stream, const char **err_msg);
 
@@ -402,10 +403,10 @@ RWKV7_API size_t rwkv7_state_entry_bytes(int32_t n_layer, int32_t n_head, int32_
  * as the ctx keeps it: d_wkv [n_layer][n_slots][n_head][64][64], d_shift_att and
  * d_shift_ffn [n_layer][n_slots][64 * n_head], 16-byte aligned (d_wkv 32).  The wkv
  * states are quantised along their rows (the key channels), the shift states kept
- * exactly.  Several pairs may read the same slot or entry.  An index out of range
- * sets bit 1 in *d_err (a device word the caller zeroed) and its pair is left out.
- * Where two of the other pairs write the same slot or entry the first is carried
- * out, the others are not, and bit 4 is set. */
+ * exactly; the cache must not overlap the pool.  Several pairs may read the same
+ * slot or entry.  An index out of range sets bit 1 in *d_err (a device word the
+ * caller zeroed) and its pair is left out.  Where two of the other pairs write the
+ * same slot or entry the first is carried out, the others are not, and bit 4 is set. */
 RWKV7_API int rwkv7_states_save(const float *d_wkv, const float *d_shift_att, const float *d_shift_ffn,
                                 int32_t n_layer, int32_t n_head, int32_t n_slots, const int32_t *d_slots,
                                 const int32_t *d_entries, int32_t n, void *d_cache, int32_t n_entries, int32_t format,

@@ -5,11 +5,11 @@
 // neighbouring values belong to one lane and a block of 32 to four, whose largest
 // value takes two shuffles.  Measured against the 6.8 TB/s of a plain copy:
 //   states   sixteen of the 2.9B shape saved and loaded as MXINT8, 885 MB: 134 us, 6.6
-//            TB/s; one 7.2B state loaded into 48 slots, 1.7 GB: 259 us, 6.6 TB/s.
+//            TB/s; one 7.2B state saved and loaded into 48 slots, 1.7 GB: 259 us, 6.6.
 //            Memory bounds them.  Stored 16 bytes a lane instead of 32 (two halves of
 //            each sector at different times) the load took 341 us.
 //   rows     4096 x 16384 bf16 to MXFP4, 170 MB: 29.7 us, 5.7 TB/s; back, 27.2 us, 6.3
-//            TB/s.  Instructions come close to bounding them (issue slots 74-80 % busy):
+//            TB/s.  Instructions come close to bounding them (issue slots 63-68 % busy):
 //            one line a warp instead of four took 59 and 45 us; for 64 x 2560 four lines
 //            a warp took 2.3 us instead of 1.6.  Four lines along a row instead of down a
 //            column tile took 28.1 us there, but 30 instead of 23 for 65536 x 300 fp16,

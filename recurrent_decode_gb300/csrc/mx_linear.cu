@@ -33,7 +33,7 @@
 // memory off the SM, so none waits for columns that a waiting CTA holds.
 //
 // What bounds it (2.07 GHz): a stage of 128 outputs x 256 tokens x 256 columns takes
-// 372 ns; its copies alone (52 KB out of L2 on every SM, 24 TB/s) take 332, its
+// 368 ns; its copies alone (52 KB out of L2 on every SM, 24 TB/s) take 332, its
 // products and powers alone 342 (253 issued back to back; waits for stages that spin
 // without ever looking at the clock give 303, but 363 together with the copies), so
 // both sides are near their limits.  5.1 PFLOP/s over a 7.2B prefill key
@@ -572,7 +572,7 @@ constexpr int MXL_XRES = 16;
 
 // Tokens of a tile and CTAs of a cluster: the pair with the least estimate of a CTA's
 // time from its first stage on, in ns.  A stage takes 250 + 0.6 nt (copies, powers and
-// products; measured 260-290 at 16 and 64 tokens, 300 at 128, 390 at 256), a tile's end
+// products; measured 290 at 16 tokens, 272 at 64, 310 at 128, 368 at 256), a tile's end
 // 5 nt alone and 1000 + 17 nt in a cluster (partial sums through shared memory).
 // Measured, chosen / next best, us: 256 x 4096 (K 4096) 64 tokens alone 9.2 / 256 tokens
 // over 4 CTAs 11.1; 256 x 1024 (K 4096) 64 over 4 7.4 / 128 over 4 8.7; 512 x 4096 128

@@ -265,8 +265,9 @@ class StateCache:
     slots_load move a ctx's slots; save and load a pool the caller owns.
 
     MXINT8 keeps every value to within 1/127 of the largest of its block of 32 along
-    a state row, MXFP4 to within 1/5; token-shift states are kept exactly.  An entry
-    that nothing was saved to holds the state of a slot after a reset."""
+    a state row, MXFP4 to within 1/5, where that is a normal number (and in MXFP4 below
+    7/8 of fp32's range); token-shift states are kept exactly.  An entry that nothing
+    was saved to holds the state of a slot after a reset."""
 
     def __init__(self, n_layer: int, n_head: int, n_entries: int, format: str = "mxint8", device=None):
         if format not in _FORMATS:
