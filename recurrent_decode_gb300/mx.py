@@ -241,9 +241,9 @@ def mx4_check(device=None):
 def _follow(stream, *tensors):
     """For a kernel that `stream` runs on tensors of the current stream: it comes after
     what that has in flight, and their memory is not handed out again before it ends."""
-    current = torch.cuda.current_stream(stream.device)
-    if current != stream:
-        stream.wait_stream(current)
+    dev = stream.device.index
+    if _raw_stream(dev) != stream.cuda_stream:
+        stream.wait_stream(torch.cuda.current_stream(dev))
         for t in tensors:
             t.record_stream(stream)
 

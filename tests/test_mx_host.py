@@ -21,7 +21,7 @@ CUDA0, CUDA1 = torch.device("cuda", 0), torch.device("cuda", 1)
 # ------------------------------------------------------------------ streams
 class Stream:
     def __init__(self, name, log, device=CUDA0):
-        self.name, self.log, self.device = name, log, device
+        self.name, self.log, self.device, self.cuda_stream = name, log, device, hash(name)
 
     def wait_stream(self, other):
         self.log.append(f"{self.name} waits for {other.name}")
@@ -54,6 +54,7 @@ class Log(list):
 def log(monkeypatch):
     log = Log()
     monkeypatch.setattr(mx, "_pair_count", lambda slots, entries, dev: 1)
+    monkeypatch.setattr(mx, "_raw_stream", lambda dev: log.current.cuda_stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: log.current)
     return log
 
