@@ -427,8 +427,9 @@ __device__ __forceinline__ void beam_pick(const BeamSelectParams &p, BeamPick &s
                 if (c != lane) mine = __ldcg(tops + c), q = __ldcg(sums + c);
                 float f, unused;
                 unpack2(exp_pair(both(fmaxf(mine, -FLT_MAX) - fmaxf(top, -FLT_MAX))), f, unused);
-                // q f, f <= 1: to a unit of 2^-40
-                sum += __umul64hi(q << 1, (unsigned long long)(f * 0x1p31f) << 32);
+                // q f, f <= 1, cut to a unit of 2^-40: f 2^63 holds all of f's bits, which stand far down where
+                // this chunk lies far below the row's top (q may be 8192 terms; of f 2^31 they took off 3e-5)
+                sum += __umul64hi(q << 1, (unsigned long long)(f * 0x1p63f));
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
