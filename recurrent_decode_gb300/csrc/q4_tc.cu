@@ -670,7 +670,9 @@ void launch_q4_tc(const Q4LinearParams &p, int xtype, cudaStream_t stream, cudaE
         a.p.x = p.room, a.p.ldx = ldt;
     }
     const auto encode = encode_fn();
-    const cuuint64_t dims[2] = {(cuuint64_t)p.w.K, (cuuint64_t)p.B}, strides[1] = {(cuuint64_t)a.p.ldx * 2};
+    // (The stride of a single row stands for nothing, and need not be one that a map takes.)
+    const int64_t ldx = p.B == 1 ? (p.w.K + 7) & ~7 : a.p.ldx;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.w.K, (cuuint64_t)p.B}, strides[1] = {(cuuint64_t)ldx * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)a.nt}, one[2] = {1, 1};
     if (!encode || encode(&a.x, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                           const_cast<void *>(a.p.x), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -157,7 +157,7 @@ def q4_linear(x, w: Q4Matrix, out=None, out_dtype=None, activation=None):
         if rows != B or cols != N or out.get_device() != dev:
             raise ValueError(f"out must be [{B}, {N}] on cuda:{dev}")
     room = None
-    if (B > FEW_ROWS or B * K > FEW_VALUES) and (ldx % 8 or x.data_ptr() % 16):  # rows off the grid are copied first
+    if (B > FEW_ROWS or B * K > FEW_VALUES) and (B > 1 and ldx % 8 or x.data_ptr() % 16):  # off the grid: copied first
         room = _room(B * (K + 7 & ~7) * 2, dev)
     _call(load_library().rwkv7_q4_linear, dev, x.data_ptr(), code, ldx, B, w.data.data_ptr(), N, K, w.group, w.zeros,
           out.data_ptr(), out_code, ldy, act, None if room is None else room.data_ptr(), _err_word(dev).data_ptr())
