@@ -449,7 +449,7 @@ RWKV7_API size_t rwkv7_beam_room_bytes(int32_t requests, int32_t width, int32_t 
  * one candidate, itself: token end_token, its own score, n = d_lengths[b]; its logits
  * are not read.  Candidates are ordered by rank, then lowest b, then lowest v; scores and ranks
  * are taken in 48 bits or more, the log of a sum to 2e-6 (of fewer than 160,000 values of any
- * kind).  A logit that is NaN or infinite, of either sign, is no
+ * kind).  Beams with equal rows of logits have equal sums, wherever the rows lie.  A logit that is NaN or infinite, of either sign, is no
  * candidate and has no weight, and a beam whose score is not finite has none at all.
  * Written, [requests][k], best first: d_tokens, d_parents (the beam b, 0 .. width - 1),
  * d_scores_out, and where not NULL d_lengths_out (n) and d_ended_out (whether the parent

@@ -135,6 +135,19 @@ struct BeamVec {
         else if constexpr (T == MX_F16) return __half2float(v);
         else return __bfloat162float(v);
     }
+    static constexpr uint32_t NONE = T == MX_F32 ? 0xFF800000u : T == MX_F16 ? 0xFC00FC00u : 0xFF80FF80u;  // -infinity
+    // Those from value c of a row of V on, c a multiple of N less what the row starts past a 16-byte boundary.
+    static __device__ __forceinline__ uint4 load(const type *x, int c, int V) {
+        if (c >= 0 && c + N <= V) return __ldcs((const uint4 *)(x + c));
+        uint32_t w[4] = {NONE, NONE, NONE, NONE};
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (c + i < 0 || c + i >= V) continue;
+            if constexpr (T == MX_F32) w[i] = ((const uint32_t *)x)[c + i];
+            else w[i / 2] = __byte_perm(w[i / 2], ((const uint16_t *)x)[c + i], i % 2 ? 0x5410 : 0x3254);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
     static __device__ __forceinline__ void up(const uint4 &w, float *v) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -165,39 +178,82 @@ struct BeamRows {  // shared memory of a chunk
     int listed;
 };
 
-// Chunk c of row r: values 256 E c - shift .. 256 E (c + 1) - shift - 1 of it, shift being
-// what the row starts past a 16-byte boundary, so that every row is read by whole vectors
-// but at its ends.
-template <int T, int E>
+// A warp's lanes' vectors w, each followed by the next lane's and the last lane's by the first one's next,
+// moved on by S words and, of 16-bit values, `bits` bits: vectors from that place on.
+template <int S, bool HALF, int n>
+__device__ __forceinline__ void beam_move(uint4 (&w)[n + 1], int lane, int bits) {
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+        const uint32_t a[4] = {w[j].x, w[j].y, w[j].z, w[j].w}, o[4] = {w[j + 1].x, w[j + 1].y, w[j + 1].z, w[j + 1].w};
+        uint32_t t[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = a[i];
+#pragma unroll
+        for (int i = 0; i < S + HALF; ++i) t[4 + i] = __shfl_sync(0xffffffffu, lane ? a[i] : o[i], (lane + 1) & 31);
+        if constexpr (HALF) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[S + i] = __funnelshift_r(t[S + i], t[S + i + 1], bits);
+        }
+        w[j] = make_uint4(t[S], t[S + 1], t[S + 2], t[S + 3]);
+    }
+}
+
+// Chunk c of row r: values 256 E c .. 256 E (c + 1) - 1 of it, 32 E in a row for a warp.  Memory is
+// read by vectors on 16-byte boundaries; where the row starts off them, the values are moved to
+// the lanes that have them in every other row, so that rows of the same values have the same
+// sums to the last bit, and equal beams the same ranks.
+template <int T, int E, bool GRID>
 __device__ __forceinline__ void beam_chunk(const BeamSelectParams &p, BeamRows &s, int row, int chunk) {
     using V = BeamVec<T>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const typename V::type *x = (const typename V::type *)p.logits + row * p.ld;
-    const int shift = (int)(((uintptr_t)x / sizeof(*x)) % V::N);
-    const int first = chunk * (BR_THREADS * E) + tid * V::N - shift;  // of the thread's first vector
-    constexpr int STEP = BR_THREADS * V::N;
+    constexpr int STEP = 32 * V::N, VECS = E / V::N;
+    const int begin = chunk * (BR_THREADS * E), first = begin + warp * (32 * E) + lane * V::N;  // of the thread's first vector
     float v[E];
-    {
-        const int begin = chunk * (BR_THREADS * E) - shift;
-        if (begin >= 0 && begin + BR_THREADS * E <= p.V) {  // whole vectors throughout
-            uint4 w[E / V::N];
+    if constexpr (GRID) {
+        if (begin + BR_THREADS * E <= p.V) {  // whole vectors throughout
+            uint4 w[VECS];
 #pragma unroll
-            for (int j = 0; j < E / V::N; ++j) w[j] = __ldcs((const uint4 *)(x + first + j * STEP));
+            for (int j = 0; j < VECS; ++j) w[j] = __ldcs((const uint4 *)(x + first + j * STEP));
 #pragma unroll
-            for (int j = 0; j < E / V::N; ++j) V::up(w[j], v + j * V::N);
+            for (int j = 0; j < VECS; ++j) V::up(w[j], v + j * V::N);
         } else {
 #pragma unroll
-            for (int j = 0; j < E / V::N; ++j) {
+            for (int j = 0; j < VECS; ++j) {
                 const int at = first + j * STEP;
-                if (at >= 0 && at + V::N <= p.V) {
+                if (at + V::N <= p.V) {
                     V::up(__ldcs((const uint4 *)(x + at)), v + j * V::N);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < V::N; ++i)
-                        v[j * V::N + i] = at + i >= 0 && at + i < p.V ? V::up(x[at + i]) : -INFINITY;
+                    for (int i = 0; i < V::N; ++i) v[j * V::N + i] = at + i < p.V ? V::up(x[at + i]) : -INFINITY;
                 }
             }
         }
+    } else {
+        const int shift = (int)(((uintptr_t)x / sizeof(*x)) % V::N);  // values past a boundary
+        uint4 w[VECS + 1];
+        const int from = begin + warp * (32 * E);
+        if (from >= shift && from + 32 * E + V::N - shift <= p.V) {  // whole vectors throughout the warp
+#pragma unroll
+            for (int j = 0; j < VECS; ++j) w[j] = __ldcs((const uint4 *)(x + first - shift + j * STEP));
+            if (lane == 0) w[VECS] = __ldcs((const uint4 *)(x + first - shift + VECS * STEP));
+        } else {
+#pragma unroll
+            for (int j = 0; j < VECS; ++j) w[j] = V::load(x, first - shift + j * STEP, p.V);
+            if (lane == 0) w[VECS] = V::load(x, first - shift + VECS * STEP, p.V);
+        }
+        constexpr bool HALF = T != MX_F32;
+        const int bits = HALF ? shift % 2 * 16 : 0;
+        switch (shift * (int)sizeof(*x) / 4) {
+        case 0:
+            if (HALF && bits) beam_move<0, HALF, VECS>(w, lane, bits);
+            break;
+        case 1: beam_move<1, HALF, VECS>(w, lane, bits); break;
+        case 2: beam_move<2, HALF, VECS>(w, lane, bits); break;
+        default: beam_move<3, HALF, VECS>(w, lane, bits);
+        }
+#pragma unroll
+        for (int j = 0; j < VECS; ++j) V::up(w[j], v + j * V::N);
     }
     float mine = v[0];
 #pragma unroll
@@ -594,7 +650,7 @@ __device__ __forceinline__ void beam_pick(const BeamSelectParams &p, BeamPick &s
     if (p.ended_out) p.ended_out[out] = ended;
 }
 
-template <int T, int E>
+template <int T, int E, bool GRID>
 __global__ void __launch_bounds__(BR_THREADS, 4) beam_select_kernel(const BeamSelectParams p) {
     __shared__ union Shared {
         BeamRows rows;
@@ -604,7 +660,7 @@ __global__ void __launch_bounds__(BR_THREADS, 4) beam_select_kernel(const BeamSe
     __shared__ bool last;
     const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks, g = row / p.W;
     // of a beam that has ended or has no score nothing is read
-    if (fabsf(p.scores[row]) < INFINITY && !(p.ended && p.ended[row])) beam_chunk<T, E>(p, s.rows, row, chunk);
+    if (fabsf(p.scores[row]) < INFINITY && !(p.ended && p.ended[row])) beam_chunk<T, E, GRID>(p, s.rows, row, chunk);
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
@@ -803,13 +859,16 @@ int beam_done(const char **err_msg, const char *what, cudaError_t e) {
     return RWKV7_ECUDA;
 }
 
-constexpr int BEAM_SHORT = 8, BEAM_LONG = 32;  // values of a thread of beam_rows_kernel
-// shift: what rows may start past a 16-byte boundary, at most.
-int beam_chunks(int V, int each, int shift = 7) { return (V + shift + BR_THREADS * each - 1) / (BR_THREADS * each); }
+constexpr int BEAM_SHORT = 8, BEAM_LONG = 32;  // values of a thread of beam_select_kernel
+int beam_chunks(int V, int each) { return (V + BR_THREADS * each - 1) / (BR_THREADS * each); }
 
-template <int T>
+template <int T, bool GRID>
 const void *beam_select_fn(bool longer) {
-    return longer ? (const void *)beam_select_kernel<T, BEAM_LONG> : (const void *)beam_select_kernel<T, BEAM_SHORT>;
+    return longer ? (const void *)beam_select_kernel<T, BEAM_LONG, GRID> : (const void *)beam_select_kernel<T, BEAM_SHORT, GRID>;
+}
+template <int T>
+const void *beam_select_fn(bool longer, bool grid) {
+    return grid ? beam_select_fn<T, true>(longer) : beam_select_fn<T, false>(longer);
 }
 
 bool share(const void *a, size_t an, const void *b, size_t bn) {
@@ -851,7 +910,8 @@ size_t rwkv7_beam_room_bytes(int32_t requests, int32_t width, int32_t vocab, int
     if (requests < 0 || width < 1 || width > BEAM_MAX_WIDTH || vocab < 1 || vocab > RWKV7_MX_MAX_DIM || k < 1 ||
         k > BEAM_MAX_K || requests > RWKV7_MX_MAX_DIM / width)
         return 0;
-    return (size_t)requests * width * beam_chunks(vocab, BEAM_SHORT) * (8 * (size_t)k + 12) + 16;
+    // (For seven values more than there are: a size that callers know by now.)
+    return (size_t)requests * width * beam_chunks(vocab + 7, BEAM_SHORT) * (8 * (size_t)k + 12) + 16;
 }
 
 int rwkv7_beam_select(const void *d_logits, int32_t dtype, int64_t ld, int32_t requests, int32_t width, int32_t vocab,
@@ -915,10 +975,8 @@ int rwkv7_beam_select(const void *d_logits, int32_t dtype, int64_t ld, int32_t r
     // fewer than the SMs, the latter spread a row over more of them.  us with the longer / shorter ones: 32
     // rows of 65,536 values 10.8 / 13.0, 256 rows of 8,000 10.0 / 13.0, 256 rows of 2,000 (one
     // chunk either way) 9.9 / 8.2.
-    const bool grid = (uintptr_t)d_logits % 16 == 0 && (rows == 1 || ld * size % 16 == 0);
-    const int shift = grid ? 0 : 16 / size - 1;
-    const bool longer = beam_chunks(vocab, BEAM_SHORT, shift) > 1 && rows * beam_chunks(vocab, BEAM_LONG, shift) >= 152;
-    p.chunks = beam_chunks(vocab, longer ? BEAM_LONG : BEAM_SHORT, shift);
+    const bool longer = beam_chunks(vocab, BEAM_SHORT) > 1 && rows * beam_chunks(vocab, BEAM_LONG) >= 152;
+    p.chunks = beam_chunks(vocab, longer ? BEAM_LONG : BEAM_SHORT);
     const int64_t lists = rows * p.chunks;
     p.tickets = d_tickets;
     p.keys = static_cast<unsigned long long *>(d_room);
@@ -928,9 +986,12 @@ int rwkv7_beam_select(const void *d_logits, int32_t dtype, int64_t ld, int32_t r
     cfg.gridDim = dim3((unsigned)lists);
     cfg.blockDim = dim3(BR_THREADS);
     cfg.stream = static_cast<cudaStream_t>(cuda_stream);
-    const void *fn = dtype == RWKV7_F32   ? beam_select_fn<MX_F32>(longer)
-                     : dtype == RWKV7_F16 ? beam_select_fn<MX_F16>(longer)
-                                          : beam_select_fn<MX_BF16>(longer);
+    // Where every row is on the 16-byte grid, a kernel that moves nothing: 256 rows of 65,536 fp32 values 26.8 us,
+    // 28.7 by the other, which takes 31.7 for 65,537; 256 of 65,536 and of 65,535 fp16 values 26.3 and 27.5.
+    const bool grid = (uintptr_t)d_logits % 16 == 0 && (rows == 1 || ld * size % 16 == 0);
+    const void *fn = dtype == RWKV7_F32   ? beam_select_fn<MX_F32>(longer, grid)
+                     : dtype == RWKV7_F16 ? beam_select_fn<MX_F16>(longer, grid)
+                                          : beam_select_fn<MX_BF16>(longer, grid);
     void *args[] = {&p};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
     return beam_done(err_msg, "selecting beams", e);
