@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(32 * QR_WARPS, 1) q4_rows_kernel(const __grid_
     const Q4Matrix &m = p.w;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int r0 = (int)((int64_t)m.rt * blockIdx.x / gridDim.x), R = (int)((int64_t)m.rt * (blockIdx.x + 1) / gridDim.x) - r0;
-    const int b0 = blockIdx.y * 8 * NT, B = min(8 * NT, p.B - b0);
+    const int B = p.B;  // 8 NT at most
     const uint32_t base = smem_u32(smem), ring = base + warp * RING, mine = ring + lane * 16;
     float *slots = (float *)(smem + a.slots), *sums = (float *)(smem + a.sums);
     // Where a lane's x lies: a row's 128 columns are 256 bytes, the 64 of every second 32 columns
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(32 * QR_WARPS, 1) q4_rows_kernel(const __grid_
         // x of these columns
         for (int i = tid; i < kc * 16 * B; i += 32 * QR_WARPS) {
             const int kt = i / (16 * B), q = i - kt * 16 * B, row = q >> 4, col = (k0 + kt) * Q4_COLS + (q & 15) * 8;
-            const uint16_t *x = (const uint16_t *)p.x + (int64_t)(b0 + row) * p.ldx;
+            const uint16_t *x = (const uint16_t *)p.x + row * p.ldx;
             const uint32_t to = a.xat + (uint32_t)(kt * B + row) * 256 + ((q & 15) ^ (row & 1) * 4) * 16;
             if (p.xvec && col + 8 <= m.K) cp16(base + to, x + col);
             else *(uint4 *)(smem + to) = q4_x8(x, col, m.K);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(32 * QR_WARPS, 1) q4_rows_kernel(const __grid_
                     continue;
                 }
             }
-            if (r0 * 16 + n < m.N) q4_store(p, b0 + b, r0 * 16 + n, v);
+            if (r0 * 16 + n < m.N) q4_store(p, b, r0 * 16 + n, v);
         }
         if (c + 1 < a.chunks) __syncthreads();
     }
@@ -235,6 +235,7 @@ static const void *q4_rows_fn(int group, bool zero) {
 }
 
 void launch_q4_rows(const Q4LinearParams &p, int xtype, cudaStream_t stream, cudaError_t *e) {
+    static_assert(RWKV7_Q4_FEW_ROWS == 16, "two tiles of eight rows of x at most");
     const int nt = p.B <= 8 ? 1 : 2, group = p.w.group;
     const bool zero = p.w.zeros != 0, bf = xtype == MX_BF16;
     const void *fn = nt == 1 ? (bf ? q4_rows_fn<true, 1>(group, zero) : q4_rows_fn<false, 1>(group, zero))
@@ -243,7 +244,7 @@ void launch_q4_rows(const Q4LinearParams &p, int xtype, cudaStream_t stream, cud
     Q4RowsArgs a;
     memset(&a, 0, sizeof a);
     a.p = p;
-    const int B = p.B < 8 * nt ? p.B : 8 * nt, limit = 32 / nt;
+    const int B = p.B, limit = 32 / nt;
     const int ctas = p.w.rt < 152 ? p.w.rt : 152 * ((p.w.rt + 152 * limit - 1) / (152 * limit));
     a.rows = (p.w.rt + ctas - 1) / ctas;
     const uint32_t part = 512u * nt;
@@ -260,7 +261,7 @@ void launch_q4_rows(const Q4LinearParams &p, int xtype, cudaStream_t stream, cud
     const uint32_t end = a.xat + (uint32_t)a.chunk * 256 * B;
     a.sums = end;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((p.B + 8 * nt - 1) / (8 * nt)));
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(32 * QR_WARPS);
     cfg.dynamicSmemBytes = end + (a.chunks > 1 ? all : 0);
     cfg.stream = stream;
