@@ -497,8 +497,9 @@ RWKV7_API int rwkv7_slots_reorder(rwkv7_ctx *ctx, const int32_t *d_slots, const 
 RWKV7_API size_t rwkv7_q4_bytes(int64_t rows, int64_t cols, int32_t group, int32_t zeros);
 
 /* Lay out a matrix: d_values [rows][cols] one code a byte (its low four bits), d_scales
- * fp16 and d_zeros bytes (NULL: none) [rows][ceil(cols / group)], row strides ldv, lds and ldz
- * elements, into d_q4 (16-byte aligned, over none of them). */
+ * fp16 and d_zeros bytes (their low four bits too; NULL: none) [rows][ceil(cols / group)], row
+ * strides ldv, lds and ldz elements, into d_q4 (16-byte aligned, over none of them).  A zero
+ * of 16, as checkpoints that keep zero - 1 can stand for, does not fit: it would be 0. */
 RWKV7_API int rwkv7_q4_pack(const uint8_t *d_values, int64_t ldv, const void *d_scales, int64_t lds,
                             const uint8_t *d_zeros, int64_t ldz, int64_t rows, int64_t cols, int32_t group, void *d_q4,
                             void *cuda_stream, const char **err_msg);

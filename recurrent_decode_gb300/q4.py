@@ -100,8 +100,10 @@ def _strided(t, dtype, rows, cols, device, what):
 
 def q4_pack(values, scales, zeros=None, group: int = 128) -> Q4Matrix:
     """Lay out a matrix from a checkpoint's parts (rwkv7_q4_pack): values [rows, cols] uint8,
-    a code 0 .. 15 each; scales float16 and zeros uint8 (None: all 8) [rows, ceil(cols /
-    group)].  Row strides are free.  The matrix stands for scale * (value - zero)."""
+    a code 0 .. 15 each; scales float16 and zeros uint8 0 .. 15 (None: all 8) [rows, ceil(cols /
+    group)].  Of values and zeros the low four bits count, so that a zero of 16 (of a
+    checkpoint that keeps zero - 1) would be 0: such a matrix does not fit.  Row strides are
+    free.  The matrix stands for scale * (value - zero)."""
     if not isinstance(values, torch.Tensor) or values.dtype is not torch.uint8 or not values.is_cuda or values.dim() != 2:
         raise TypeError("values must be a two-dimensional uint8 CUDA tensor")
     rows, cols = values.shape
