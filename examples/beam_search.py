@@ -6,8 +6,9 @@ the same choice of tokens from a head in 4 bits.
 1. Every prompt is prefilled once, its state forked to `width` slots, and beam_search keeps
    the best beams for a number of steps.  Printed: the best beam's summed log-probability and the
    greedy continuation's.
-2. Rows as the final LayerNorm gives them go through the head in fp16 and in 4 bits with a scale
-   for 64 columns (q4_quantize once, q4_linear a step), and beam_select picks from both.
+2. Random rows, normed as the final LayerNorm's are, go through the head in fp16 and in 4 bits with a
+   scale for 64 columns (q4_quantize once, q4_linear a step), and beam_select picks from both.  (The decode
+   step computes its head itself, in fp16; the search above does not use this one.)
    Printed: bytes of both heads, how far the logits are, how many picks agree.
 """
 import argparse

@@ -507,7 +507,7 @@ RWKV7_API int rwkv7_q4_pack(const uint8_t *d_values, int64_t ldv, const void *d_
 /* Quantise rows (as for rwkv7_mx4_quantize).  Without zeros the scale is a group's max |x| / 7
  * rounded to fp16 and q = 8 + x / scale to the nearest, ties to even, kept in 0 .. 15; with
  * them, from low = min(x, 0) and high = max(x, 0), the scale is (high - low) / 15 rounded to
- * fp16, zero = -low / scale and q = zero + x / scale, likewise.  A scale past fp16's
+ * fp16, zero = -low / scale and q = zero plus x / scale to the nearest, likewise.  A scale past fp16's
  * largest number is that number; a scale of 0 stands for a group of zeros.  A group with an
  * infinity or NaN reads back as NaN. */
 RWKV7_API int rwkv7_q4_quantize(const void *d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t group,

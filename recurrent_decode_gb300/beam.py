@@ -179,7 +179,7 @@ def beam_search(ctx, prompts, width: int, n_out: int, *, end_token: int | None =
     where the beam ended.  prompts: int32 arrays of at least one token.  A prompt's body is
     prefilled once into one slot; its beams' states are forked from there and moved with
     rwkv7_slots_reorder.  slots: the slots to use, width for each prompt (default: the
-    context's first); they are reset first, and hold the last beams' states afterwards.
+    context's first); what they held is lost, and they hold the last beams' states afterwards.
 
     Every step is decode_step, beam_select and slots_reorder on the context's stream; the
     host waits once, at the end."""

@@ -24,10 +24,10 @@
 // took norms and ranks by it 12 us): the candidates' scores are pairs of fp32, high and low part,
 // unless a score or what a length divides it by is out of their range.
 //
-// Measured (device time; by bytes at the copy rate): 4 rows of 65,536 fp32 logits 7 us (0.15), 64 rows
-// 11 (2.5), 192 rows 26 (7.4).  What is left is latency: a chunk's loads, its three
+// Measured (in a graph, with the 1 us that zeroes its tickets; by bytes at the copy rate): 4 rows of 65,536 fp32
+// logits 8 us (0.15), 64 rows 12 (2.5), 192 rows 25 (7.4).  What is left is latency: a chunk's loads, its three
 // barriers and its ticket follow one another, and the four CTAs that an SM's registers hold do not
-// cover them (29 % of issue slots, 2.9 rounds of chunks of 8192 values).  Chunks of 4096: 37 us.
+// cover them (23 % of issue slots, 2.5 rounds of chunks of 8192 values).  Chunks of 4096: 37 us.
 #include <cfloat>
 #include <cstdio>
 #include <cstring>

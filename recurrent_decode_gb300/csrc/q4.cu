@@ -559,10 +559,11 @@ int rwkv7_q4_linear(const void *d_x, int32_t x_dtype, int64_t ldx, int64_t B, co
     p.room = d_room, p.err = d_err;
     cudaError_t e = cudaSuccess;
     // Up to 16 rows a warp's own products keep up with the memory; x in every SM's shared memory is what
-    // they pay.  Past 256 KB of it (taken in turns), where the other kernel needs no second round of tiles,
-    // that one is faster: us by warps / by tcgen05, 4096 x 16384 in groups of 128: 4 rows 13.1 / 16.8, 8 rows
-    // 17.6 / 16.9, 12 rows 23.7 / 17.3; 2560 x 10240, 64: 8 rows 11.7 / 11.7, 16 rows 19.9 / 12.0; 16384 x
-    // 4096, 16 rows: 128: 18.9 / 16.3, 64: 18.6 / 19.0; 65536 x 2560, 64: 16 rows 35.3 / 42.8.
+    // they pay, copied by each and taken in turns from 80 to 110 KB on.  Past 256 KB of it the other kernel is
+    // faster, unless it needs a second round of tiles: us by warps / by tcgen05, 4096 x 16384 in groups of 128: 4 rows
+    // 13.1 / 16.8, 8 rows 17.6 / 16.9, 12 rows 23.7 / 17.3; 2560 x 10240, 64: 8 rows 11.7 / 11.7, 16 rows 19.9 /
+    // 12.0; 65536 x 2560, 64: 16 rows 35.3 / 42.8.  Near the border the sizes alone do not tell: 128 KB of x by
+    // 16384 x 4096, 16 rows, takes 18.9 / 16.3 in groups of 128 and 18.6 / 19.0 in groups of 64, by warps either way.
     if (B <= RWKV7_Q4_FEW_ROWS && (B * K <= RWKV7_Q4_FEW_VALUES || N > 152 * 128)) {
         launch_q4_rows(p, x_dtype, static_cast<cudaStream_t>(cuda_stream), &e);
     } else {
